@@ -10,6 +10,10 @@ The function names are those of the C ABI:
 * ``lily_q4_moe_decode(layer, x, y, topk_idx=None, topk_w=None, ws=None, stream=None)``
 * ``lily_q4_moe_prefill(layer, x, y, topk_idx=None, topk_w=None, ws=None, stream=None)``
 * ``lily_q4_gemv_argmax(W, x, token, logits=None, ws=None, stream=None)``
+* ``lily_qk_norm_rope(op, q, k, pos, q_out, k_out, stream=None)`` with ``lily_rope_turns``;
+* ``lily_kv8_append(cache, batch, k, v, ws=None, stream=None)``, ``lily_kv8_read(...)``;
+* ``lily_kv8_attention(cache, batch, q, out, scale, lse=None, causal=True, window=0, ws=None,
+  stream=None)`` with ``lily_kv8_attention_workspace_bytes``;
 * ``lily_q4_moe_workspace_bytes``, ``lily_q4_gemv_argmax_workspace_bytes``,
   ``lily_q4_workspace_init``, ``lily_q4_workspace_status``,
   ``lily_q4_status_string``, ``lily_q4_pack``, ``lily_q4_unpack``.
@@ -34,6 +38,10 @@ ERR_UNSUPPORTED = -2
 ERR_WORKSPACE_TOO_SMALL = -3
 ERR_CUDA = -4
 ERR_TIMEOUT = -5
+ERR_INDEX = -6
+
+BF16, F16, F32 = 0, 1, 2
+ROPE_SCALING = {"none": 0, "linear": 1, "yarn": 2}
 
 
 class Q4Error(RuntimeError):
@@ -56,6 +64,25 @@ class lily_q4_moe_layer(C.Structure):
                 ("shared_gate", C.c_void_p),
                 ("shared_bits", C.c_int32), ("router_bits", C.c_int32),
                 ("router_q8", lily_q4_mat)]
+
+
+class lily_qk_rope(C.Structure):
+    _fields_ = [("head_dim", C.c_int32), ("rotary_dim", C.c_int32), ("interleaved", C.c_int32),
+                ("dtype", C.c_int32), ("normalize", C.c_int32), ("eps", C.c_float),
+                ("weight_offset", C.c_float), ("rope_scale", C.c_float),
+                ("q_weight", C.c_void_p), ("k_weight", C.c_void_p), ("turns", C.c_void_p)]
+
+
+class lily_kv8_cache(C.Structure):
+    _fields_ = [("k", C.c_void_p), ("v", C.c_void_p), ("k_amax", C.c_void_p),
+                ("v_amax", C.c_void_p), ("n_pages", C.c_int32), ("kv_heads", C.c_int32),
+                ("page", C.c_int32), ("head_dim", C.c_int32)]
+
+
+class lily_kv8_batch(C.Structure):
+    _fields_ = [("block_table", C.c_void_p), ("q_start", C.c_void_p), ("kv_len", C.c_void_p),
+                ("table_pages", C.c_int32), ("batch", C.c_int32), ("max_q", C.c_int32),
+                ("max_kv", C.c_int32)]
 
 
 _lib = None
@@ -94,7 +121,20 @@ def load(path: Optional[str] = None):
     L.lily_q4_status_string.restype = C.c_char_p
     L.lily_q4_pack.argtypes = [vp, i32, i32, vp]
     L.lily_q4_unpack.argtypes = [vp, i32, i32, vp]
-    for f in ("lily_q4_moe_decode", "lily_q4_moe_prefill", "lily_q4_gemv_argmax",
+    i64, f64, rows = C.c_int64, C.c_double, [vp, C.c_int64, C.c_int64]
+    cache, batch = C.POINTER(lily_kv8_cache), C.POINTER(lily_kv8_batch)
+    L.lily_rope_turns.argtypes = [i32, f64, i32, f64, f64, f64, f64, vp]
+    L.lily_qk_norm_rope.argtypes = [C.POINTER(lily_qk_rope), i32, i32, i32, vp, *rows, *rows, *rows,
+                                    *rows, vp]
+    L.lily_kv8_append.argtypes = [cache, batch, i32, i32, *rows, *rows, vp, sz, vp]
+    L.lily_kv8_read.argtypes = L.lily_kv8_append.argtypes
+    L.lily_kv8_attention.argtypes = [cache, batch, i32, i32, i32, C.c_float, i32, i32, *rows, *rows,
+                                     vp, vp, sz, vp]
+    L.lily_kv8_attention_workspace_bytes.argtypes = [cache, batch, i32, i32]
+    L.lily_kv8_attention_workspace_bytes.restype = sz
+    for f in ("lily_rope_turns", "lily_qk_norm_rope", "lily_kv8_append", "lily_kv8_read",
+              "lily_kv8_attention",
+              "lily_q4_moe_decode", "lily_q4_moe_prefill", "lily_q4_gemv_argmax",
               "lily_q4_workspace_init", "lily_q4_workspace_status", "lily_q4_pack",
               "lily_q4_unpack", "lily_q4_version", "lily_q4_moe_launches",
               "lily_q4_gemv_argmax_noalloc", "lily_q4_gemv_argmax_noalloc_status",
@@ -137,10 +177,11 @@ def _stream(stream):
 
 
 def to_device(a: np.ndarray, device="cuda"):
-    """Upload a numpy array (uint16/uint32/float32/int32) as a torch tensor of the same bits."""
+    """Upload a numpy array (uint16/uint32/uint64/float32/int32) as a torch tensor of the same bits."""
     torch = _torch()
     a = np.ascontiguousarray(a)
-    view = {np.dtype(np.uint16): np.int16, np.dtype(np.uint32): np.int32}.get(a.dtype)
+    view = {np.dtype(np.uint16): np.int16, np.dtype(np.uint32): np.int32,
+            np.dtype(np.uint64): np.int64}.get(a.dtype)
     if view is not None:
         a = a.view(view)
     return torch.from_numpy(a).to(device)
@@ -349,3 +390,182 @@ def lily_q4_unpack(w: np.ndarray, N: int, K: int) -> np.ndarray:
     q = np.empty((N, K), dtype=np.uint8)
     _check(load().lily_q4_unpack(w.ctypes.data, N, K, q.ctypes.data), "lily_q4_unpack")
     return q
+
+
+# --------------------------------------------------------------------------- attention operators
+
+def _dtype_code(t, what, f32=False):
+    """bf16 tensors (or their bits as int16, as elsewhere in this binding), fp16, fp32 if allowed."""
+    name = str(t.dtype)
+    code = {"torch.bfloat16": BF16, "torch.int16": BF16, "torch.float16": F16}.get(name)
+    if code is None and f32 and name == "torch.float32":
+        code = F32
+    if code is None:
+        raise Q4Error(ERR_UNSUPPORTED, f"{what}: dtype {name}")
+    return code
+
+
+def _require(ok, what):
+    if not ok:
+        raise Q4Error(ERR_INVALID_ARG, what)
+
+
+def _rows(t, heads, dim, what):
+    """(pointer, token stride, head stride) of a [T, heads, dim] tensor with a dense last axis."""
+    _require(t.dim() == 3 and t.shape[2] == dim and (heads is None or t.shape[1] == heads)
+             and (t.stride(2) == 1 or t.numel() == 0), f"{what}: shape {tuple(t.shape)}")
+    return t.data_ptr(), t.stride(0), t.stride(1)
+
+
+def _int32(t, what):
+    _require(str(t.dtype) == "torch.int32" and t.is_contiguous(), f"{what}: contiguous int32")
+    return t.data_ptr()
+
+
+def lily_rope_turns(rotary_dim: int, base: float = 10000.0, scaling: str = "none",
+                    factor: float = 1.0, original_len: float = 1.0, slow: float = 1.0,
+                    fast: float = 32.0) -> np.ndarray:
+    """The rotation table of lily_qk_norm_rope: uint64 [rotary_dim / 2] fractions of a turn for
+    each position step (host only); see include/lily_q4.h.  ``to_device`` uploads it."""
+    _require(scaling in ROPE_SCALING, f"lily_rope_turns: scaling {scaling!r}")
+    turns = np.zeros(max(int(rotary_dim), 0) // 2, dtype=np.uint64)
+    _check(load().lily_rope_turns(int(rotary_dim), float(base), ROPE_SCALING[scaling], float(factor),
+                                  float(original_len), float(slow), float(fast), turns.ctypes.data),
+           "lily_rope_turns")
+    return turns
+
+
+class QKNormRope:
+    """The constants of lily_qk_norm_rope: weights and table on the GPU, and the C struct."""
+
+    def __init__(self, head_dim, rotary_dim, turns, q_weight=None, k_weight=None, eps=1e-6,
+                 interleaved=False, weight_offset=0.0, rope_scale=1.0, normalize=True):
+        self.head_dim, self.rotary_dim = int(head_dim), int(rotary_dim)
+        self.turns, self.q_weight, self.k_weight = turns, q_weight, k_weight
+        self.dtype = None
+        for w in (q_weight, k_weight):
+            if w is None:
+                continue
+            _require(w.numel() == head_dim and w.is_contiguous(), "QKNormRope: weights of one head")
+            code = _dtype_code(w, "QKNormRope")
+            _require(self.dtype in (None, code), "QKNormRope: weights of two types")
+            self.dtype = code
+        if rotary_dim:
+            _require(turns is not None and turns.numel() * turns.element_size() == 4 * rotary_dim
+                     and turns.is_contiguous(), "QKNormRope: turns is uint64 [rotary_dim / 2]")
+        self._c = lily_qk_rope(self.head_dim, self.rotary_dim, int(bool(interleaved)),
+                               self.dtype or 0, int(bool(normalize)), float(eps),
+                               float(weight_offset), float(rope_scale), _ptr(q_weight),
+                               _ptr(k_weight), _ptr(turns) if rotary_dim else None)
+
+    def c(self, dtype) -> lily_qk_rope:
+        _require(self.dtype in (None, dtype), "lily_qk_norm_rope: weights and heads of two types")
+        self._c.dtype = dtype
+        return self._c
+
+
+def lily_qk_norm_rope(op: QKNormRope, q, k, pos, q_out, k_out, stream=None):
+    """Norm and rotation of every head of q [T, q_heads, D] and k [T, k_heads, D] (views with any
+    token and head strides) into q_out and k_out, which may be q and k; k may be None."""
+    T, d = int(q.shape[0]), op.head_dim
+    dtype = _dtype_code(q, "lily_qk_norm_rope")
+    _require(q_out.dtype == q.dtype and q_out.shape == q.shape, "lily_qk_norm_rope: q_out")
+    heads, kr, ko = 0, (None, 0, 0), (None, 0, 0)
+    if k is not None:
+        _require(k.dtype == q.dtype and k_out.dtype == q.dtype and k_out.shape == k.shape
+                 and k.shape[0] == T, "lily_qk_norm_rope: k, k_out")
+        heads, kr, ko = int(k.shape[1]), _rows(k, None, d, "k"), _rows(k_out, None, d, "k_out")
+    if op.rotary_dim:
+        _require(pos.numel() == T, "lily_qk_norm_rope: pos")
+        pos = _int32(pos, "pos")
+    else:
+        pos = None
+    return _check(load().lily_qk_norm_rope(C.byref(op.c(dtype)), T, int(q.shape[1]), heads, pos,
+                                           *_rows(q, None, d, "q"), *_rows(q_out, None, d, "q_out"),
+                                           *kr, *ko, _stream(stream)), "lily_qk_norm_rope")
+
+
+class KV8Cache:
+    """A paged 8-bit key/value cache on the GPU: int8 codes [pages, kv_heads, page, head_dim] and
+    fp32 magnitudes [pages, kv_heads] of the keys and of the values."""
+
+    def __init__(self, k, v, k_amax, v_amax):
+        _require(k.dim() == 4 and v.shape == k.shape and str(k.dtype) == str(v.dtype) == "torch.int8"
+                 and k.is_contiguous() and v.is_contiguous(), "KV8Cache: codes")
+        for a in (k_amax, v_amax):
+            _require(tuple(a.shape) == tuple(k.shape[:2]) and str(a.dtype) == "torch.float32"
+                     and a.is_contiguous(), "KV8Cache: magnitudes")
+        self.k, self.v, self.k_amax, self.v_amax = k, v, k_amax, v_amax
+        self.n_pages, self.kv_heads, self.page, self.head_dim = (int(n) for n in k.shape)
+        self._c = lily_kv8_cache(_ptr(k), _ptr(v), _ptr(k_amax), _ptr(v_amax), self.n_pages,
+                                 self.kv_heads, self.page, self.head_dim)
+
+    @classmethod
+    def new(cls, n_pages, kv_heads, page, head_dim, device="cuda"):
+        torch = _torch()
+        codes = [torch.zeros((n_pages, kv_heads, page, head_dim), dtype=torch.int8, device=device)
+                 for _ in range(2)]
+        amax = [torch.zeros((n_pages, kv_heads), dtype=torch.float32, device=device)
+                for _ in range(2)]
+        return cls(*codes, *amax)
+
+    def c(self) -> lily_kv8_cache:
+        return self._c
+
+
+class KV8Batch:
+    """The sequences of a call: block_table int32 [batch, pages], q_start int32 [batch + 1],
+    kv_len int32 [batch], all on the GPU, and the host's bounds of rows and tokens a sequence."""
+
+    def __init__(self, block_table, q_start, kv_len, max_q, max_kv):
+        n = int(kv_len.numel())
+        _require(block_table.dim() == 2 and block_table.shape[0] == n and q_start.numel() == n + 1,
+                 "KV8Batch: block_table [batch, pages], q_start [batch + 1], kv_len [batch]")
+        self.block_table, self.q_start, self.kv_len = block_table, q_start, kv_len
+        self._c = lily_kv8_batch(_int32(block_table, "block_table"), _int32(q_start, "q_start"),
+                                 _int32(kv_len, "kv_len"), int(block_table.shape[1]), n, int(max_q),
+                                 int(max_kv))
+
+    def c(self) -> lily_kv8_batch:
+        return self._c
+
+
+def _kv8_rows(fn, name, cache, batch, k, v, ws, stream, f32):
+    T, h, d = int(k.shape[0]), cache.kv_heads, cache.head_dim
+    dtype = _dtype_code(k, name, f32)
+    _require(v.dtype == k.dtype and v.shape[0] == T, f"{name}: k and v")
+    return _check(fn(C.byref(cache.c()), C.byref(batch.c()), T, dtype, *_rows(k, h, d, "k"),
+                     *_rows(v, h, d, "v"), _ptr(ws), ws.numel() if ws is not None else 0,
+                     _stream(stream)), name)
+
+
+def lily_kv8_append(cache: KV8Cache, batch: KV8Batch, k, v, ws=None, stream=None):
+    """Writes the batch's tokens k, v [T, kv_heads, head_dim] into the cache; see include/lily_q4.h."""
+    return _kv8_rows(load().lily_kv8_append, "lily_kv8_append", cache, batch, k, v, ws, stream, False)
+
+
+def lily_kv8_read(cache: KV8Cache, batch: KV8Batch, k_out, v_out, ws=None, stream=None):
+    """The values of the batch's tokens into k_out, v_out (bf16, fp16 or fp32)."""
+    return _kv8_rows(load().lily_kv8_read, "lily_kv8_read", cache, batch, k_out, v_out, ws, stream, True)
+
+
+def lily_kv8_attention_workspace_bytes(cache: KV8Cache, batch: KV8Batch, T: int, q_heads: int) -> int:
+    return int(load().lily_kv8_attention_workspace_bytes(C.byref(cache.c()), C.byref(batch.c()),
+                                                         int(T), int(q_heads)))
+
+
+def lily_kv8_attention(cache: KV8Cache, batch: KV8Batch, q, out, scale, lse=None, causal=True,
+                       window=0, ws=None, stream=None):
+    """Attention of q [T, q_heads, head_dim] over the batch's cached tokens into out (same shape)
+    and, if given, lse fp32 [T, q_heads]; see include/lily_q4.h."""
+    T, heads, d = int(q.shape[0]), int(q.shape[1]), cache.head_dim
+    dtype = _dtype_code(q, "lily_kv8_attention")
+    _require(out.dtype == q.dtype and out.shape == q.shape, "lily_kv8_attention: out")
+    if lse is not None:
+        _require(lse.numel() == T * heads and str(lse.dtype) == "torch.float32"
+                 and lse.is_contiguous(), "lily_kv8_attention: lse is fp32 [T, q_heads]")
+    return _check(load().lily_kv8_attention(C.byref(cache.c()), C.byref(batch.c()), T, heads, dtype,
+                                            float(scale), int(bool(causal)), int(window),
+                                            *_rows(q, heads, d, "q"), *_rows(out, heads, d, "out"),
+                                            _ptr(lse), _ptr(ws), ws.numel() if ws is not None else 0,
+                                            _stream(stream)), "lily_kv8_attention")

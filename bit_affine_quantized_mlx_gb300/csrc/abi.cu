@@ -1,6 +1,7 @@
 // C-ABI entry points of liblily_q4: argument validation, workspace sizing and the
 // host-only format helpers.  Compute is enqueued by the launchers in the other
 // translation units; nothing here allocates device memory.
+#include <cmath>
 #include <cstring>
 
 #include "internal.h"
@@ -68,6 +69,52 @@ static int check_io(const uint16_t *x, uint16_t *y, int32_t *idx, float *w, void
   return LILY_Q4_OK;
 }
 
+// ---------------------------------------------------------------- attention operators
+static bool rows_ok(const Rows &r, int elem_bytes) {
+  const int64_t step = 16 / elem_bytes;
+  return r.p && aligned(r.p, 16) && r.ts % step == 0 && r.hs % step == 0;
+}
+
+static int check_cache(const lily_kv8_cache *C) {
+  if (!C || !C->k || !C->v || !C->k_amax || !C->v_amax) return LILY_Q4_ERR_INVALID_ARG;
+  if (!aligned(C->k, 16) || !aligned(C->v, 16) || !aligned(C->k_amax, 4) || !aligned(C->v_amax, 4))
+    return LILY_Q4_ERR_INVALID_ARG;
+  if (C->n_pages <= 0 || C->kv_heads <= 0 || C->kv_heads > 65535) return LILY_Q4_ERR_INVALID_ARG;
+  if (C->page != 16 && C->page != 32 && C->page != 64 && C->page != 128) return LILY_Q4_ERR_UNSUPPORTED;
+  if (C->head_dim != 64 && C->head_dim != 128 && C->head_dim != 256) return LILY_Q4_ERR_UNSUPPORTED;
+  return LILY_Q4_OK;
+}
+
+// Bounds only: what sizes a workspace.
+static int check_bounds(const lily_kv8_batch *b, int T) {
+  if (!b || T < 0 || b->batch < 0 || b->table_pages < 0 || b->max_q < 0 || b->max_kv < 0)
+    return LILY_Q4_ERR_INVALID_ARG;
+  if (b->batch > 4096) return LILY_Q4_ERR_UNSUPPORTED;
+  if (T > 0 && (b->batch == 0 || b->table_pages == 0 || b->max_q == 0)) return LILY_Q4_ERR_INVALID_ARG;
+  return LILY_Q4_OK;
+}
+
+static int check_batch(const lily_kv8_batch *b, int T, void *ws, size_t ws_bytes) {
+  const int rc = check_bounds(b, T);
+  if (rc != LILY_Q4_OK) return rc;
+  if (T == 0) return LILY_Q4_OK;
+  if (!b->block_table || !b->q_start || !b->kv_len) return LILY_Q4_ERR_INVALID_ARG;
+  if (!aligned(b->block_table, 4) || !aligned(b->q_start, 4) || !aligned(b->kv_len, 4))
+    return LILY_Q4_ERR_INVALID_ARG;
+  if (!ws || !aligned(ws, kAlign)) return LILY_Q4_ERR_INVALID_ARG;
+  return ws_bytes < kAlign ? LILY_Q4_ERR_WORKSPACE_TOO_SMALL : LILY_Q4_OK;
+}
+
+static int check_attention(const lily_kv8_cache *C, const lily_kv8_batch *b, int T, int q_heads) {
+  int rc = check_cache(C);
+  if (rc != LILY_Q4_OK) return rc;
+  rc = check_bounds(b, T);
+  if (rc != LILY_Q4_OK) return rc;
+  if (q_heads <= 0 || q_heads % C->kv_heads) return LILY_Q4_ERR_INVALID_ARG;
+  if (q_heads / C->kv_heads > 128) return LILY_Q4_ERR_UNSUPPORTED;
+  return LILY_Q4_OK;
+}
+
 }  // namespace lq4
 
 using namespace lq4;
@@ -84,6 +131,7 @@ const char *lily_q4_status_string(int status) {
     case LILY_Q4_ERR_WORKSPACE_TOO_SMALL: return "workspace too small";
     case LILY_Q4_ERR_CUDA: return "CUDA error";
     case LILY_Q4_ERR_TIMEOUT: return "device-side wait timed out";
+    case LILY_Q4_ERR_INDEX: return "length or page number out of range";
     default: return "unknown status";
   }
 }
@@ -146,15 +194,18 @@ int lily_q4_workspace_init(void *ws, size_t ws_bytes, lily_q4_stream_t stream) {
 int lily_q4_workspace_status(void *ws, lily_q4_stream_t stream) {
   if (!ws || !aligned(ws, kAlign)) return LILY_Q4_ERR_INVALID_ARG;
   cudaStream_t st = (cudaStream_t)stream;
-  int32_t word = 0;
+  int32_t hdr[kHdrIndexError + 1] = {0};
   if (cudaStreamSynchronize(st) != cudaSuccess) return LILY_Q4_ERR_CUDA;
-  if (cudaMemcpy(&word, ws, sizeof(word), cudaMemcpyDeviceToHost) != cudaSuccess)
+  if (cudaMemcpy(hdr, ws, sizeof(hdr), cudaMemcpyDeviceToHost) != cudaSuccess)
     return LILY_Q4_ERR_CUDA;
-  if (word != 0) {
-    if (cudaMemset(ws, 0, sizeof(word)) != cudaSuccess) return LILY_Q4_ERR_CUDA;
-    return LILY_Q4_ERR_TIMEOUT;
+  int rc = LILY_Q4_OK;
+  for (const int w : {kHdrIndexError, kHdrError}) {
+    if (hdr[w] == 0) continue;
+    if (cudaMemset(static_cast<int32_t *>(ws) + w, 0, sizeof(int32_t)) != cudaSuccess)
+      return LILY_Q4_ERR_CUDA;
+    rc = w == kHdrError ? LILY_Q4_ERR_TIMEOUT : LILY_Q4_ERR_INDEX;
   }
-  return LILY_Q4_OK;
+  return rc;
 }
 
 int lily_q4_selftest_timeout(void *ws, size_t ws_bytes, int32_t which, lily_q4_stream_t stream) {
@@ -240,6 +291,97 @@ int lily_q4_moe_prefill(const lily_q4_moe_layer *layer, const uint16_t *x, int32
   if (rc != LILY_Q4_OK) return rc;
   if (ws_bytes < prefill_ws_layout(*layer, T).total) return LILY_Q4_ERR_WORKSPACE_TOO_SMALL;
   return launch_moe_prefill(*layer, x, T, y, topk_idx, topk_w, ws, (cudaStream_t)stream);
+}
+
+int lily_rope_turns(int32_t rotary_dim, double base, int32_t scaling, double factor,
+                    double original_len, double slow, double fast, uint64_t *turns) {
+  if (rotary_dim < 0 || rotary_dim > 256 || rotary_dim % 2) return LILY_Q4_ERR_INVALID_ARG;
+  if (rotary_dim == 0) return LILY_Q4_OK;
+  if (!turns || !(base > 0) || !(base < HUGE_VAL)) return LILY_Q4_ERR_INVALID_ARG;
+  if (scaling != LILY_ROPE_NONE && scaling != LILY_ROPE_LINEAR && scaling != LILY_ROPE_YARN)
+    return LILY_Q4_ERR_INVALID_ARG;
+  if (scaling != LILY_ROPE_NONE && !(factor > 0 && factor < HUGE_VAL)) return LILY_Q4_ERR_INVALID_ARG;
+  if (scaling == LILY_ROPE_YARN &&
+      !(original_len > 0 && original_len < HUGE_VAL && fast > slow && fast < HUGE_VAL && slow > -HUGE_VAL))
+    return LILY_Q4_ERR_INVALID_ARG;
+  return rope_turns(rotary_dim, base, scaling, factor, original_len, slow, fast, turns);
+}
+
+int lily_qk_norm_rope(const lily_qk_rope *op, int32_t T, int32_t q_heads, int32_t k_heads,
+                      const int32_t *pos, const void *q, int64_t q_ts, int64_t q_hs, void *q_out,
+                      int64_t qo_ts, int64_t qo_hs, const void *k, int64_t k_ts, int64_t k_hs,
+                      void *k_out, int64_t ko_ts, int64_t ko_hs, lily_q4_stream_t stream) {
+  if (!op || T < 0 || q_heads < 0 || k_heads < 0) return LILY_Q4_ERR_INVALID_ARG;
+  if (op->head_dim < 8 || op->head_dim > 256 || op->head_dim % 8) return LILY_Q4_ERR_UNSUPPORTED;
+  if (op->rotary_dim < 0 || op->rotary_dim > op->head_dim || op->rotary_dim % 2)
+    return LILY_Q4_ERR_INVALID_ARG;
+  if (op->dtype != LILY_BF16 && op->dtype != LILY_F16) return LILY_Q4_ERR_UNSUPPORTED;
+  if ((op->interleaved != 0 && op->interleaved != 1) || (op->normalize != 0 && op->normalize != 1))
+    return LILY_Q4_ERR_INVALID_ARG;
+  if (op->normalize && !(op->eps >= 0.f)) return LILY_Q4_ERR_INVALID_ARG;
+  if ((op->q_weight && !aligned(op->q_weight, 16)) || (op->k_weight && !aligned(op->k_weight, 16)))
+    return LILY_Q4_ERR_INVALID_ARG;
+  if (op->rotary_dim > 0 && (!op->turns || !aligned(op->turns, 8))) return LILY_Q4_ERR_INVALID_ARG;
+  if (T == 0 || (q_heads == 0 && k_heads == 0)) return LILY_Q4_OK;
+  if (op->rotary_dim > 0 && (!pos || !aligned(pos, 4))) return LILY_Q4_ERR_INVALID_ARG;
+  const Rows qi{const_cast<void *>(q), q_ts, q_hs}, qo{q_out, qo_ts, qo_hs};
+  const Rows ki{const_cast<void *>(k), k_ts, k_hs}, ko{k_out, ko_ts, ko_hs};
+  if (q_heads && (!rows_ok(qi, 2) || !rows_ok(qo, 2))) return LILY_Q4_ERR_INVALID_ARG;
+  if (k_heads && (!rows_ok(ki, 2) || !rows_ok(ko, 2))) return LILY_Q4_ERR_INVALID_ARG;
+  return launch_qk_norm_rope(*op, T, q_heads, k_heads, pos, qi, qo, ki, ko, (cudaStream_t)stream);
+}
+
+int lily_kv8_append(const lily_kv8_cache *cache, const lily_kv8_batch *batch, int32_t T, int32_t dtype,
+                    const void *k, int64_t k_ts, int64_t k_hs, const void *v, int64_t v_ts,
+                    int64_t v_hs, void *ws, size_t ws_bytes, lily_q4_stream_t stream) {
+  int rc = check_cache(cache);
+  if (rc != LILY_Q4_OK) return rc;
+  if (dtype != LILY_BF16 && dtype != LILY_F16) return LILY_Q4_ERR_UNSUPPORTED;
+  rc = check_batch(batch, T, ws, ws_bytes);
+  if (rc != LILY_Q4_OK || T == 0) return rc;
+  const Rows kr{const_cast<void *>(k), k_ts, k_hs}, vr{const_cast<void *>(v), v_ts, v_hs};
+  if (!rows_ok(kr, 2) || !rows_ok(vr, 2)) return LILY_Q4_ERR_INVALID_ARG;
+  return launch_kv8_append(*cache, *batch, T, dtype, kr, vr, ws, (cudaStream_t)stream);
+}
+
+int lily_kv8_read(const lily_kv8_cache *cache, const lily_kv8_batch *batch, int32_t T, int32_t dtype,
+                  void *k_out, int64_t k_ts, int64_t k_hs, void *v_out, int64_t v_ts, int64_t v_hs,
+                  void *ws, size_t ws_bytes, lily_q4_stream_t stream) {
+  int rc = check_cache(cache);
+  if (rc != LILY_Q4_OK) return rc;
+  if (dtype != LILY_BF16 && dtype != LILY_F16 && dtype != LILY_F32) return LILY_Q4_ERR_UNSUPPORTED;
+  rc = check_batch(batch, T, ws, ws_bytes);
+  if (rc != LILY_Q4_OK || T == 0) return rc;
+  const Rows kr{k_out, k_ts, k_hs}, vr{v_out, v_ts, v_hs};
+  const int eb = dtype == LILY_F32 ? 4 : 2;
+  if (!rows_ok(kr, eb) || !rows_ok(vr, eb)) return LILY_Q4_ERR_INVALID_ARG;
+  return launch_kv8_read(*cache, *batch, T, dtype, kr, vr, ws, (cudaStream_t)stream);
+}
+
+size_t lily_kv8_attention_workspace_bytes(const lily_kv8_cache *cache, const lily_kv8_batch *batch,
+                                          int32_t T, int32_t q_heads) {
+  if (check_attention(cache, batch, T, q_heads) != LILY_Q4_OK) return 0;
+  return kv8_attention_ws_bytes(*cache, *batch, T, q_heads);
+}
+
+int lily_kv8_attention(const lily_kv8_cache *cache, const lily_kv8_batch *batch, int32_t T,
+                       int32_t q_heads, int32_t dtype, float scale, int32_t causal, int32_t window,
+                       const void *q, int64_t q_ts, int64_t q_hs, void *out, int64_t o_ts,
+                       int64_t o_hs, float *lse, void *ws, size_t ws_bytes, lily_q4_stream_t stream) {
+  int rc = check_attention(cache, batch, T, q_heads);
+  if (rc != LILY_Q4_OK) return rc;
+  if (dtype != LILY_BF16 && dtype != LILY_F16) return LILY_Q4_ERR_UNSUPPORTED;
+  if ((causal != 0 && causal != 1) || window < 0 || !(scale == scale) || !(fabsf(scale) < HUGE_VALF))
+    return LILY_Q4_ERR_INVALID_ARG;
+  rc = check_batch(batch, T, ws, ws_bytes);
+  if (rc != LILY_Q4_OK || T == 0) return rc;
+  const Rows qr{const_cast<void *>(q), q_ts, q_hs}, orow{out, o_ts, o_hs};
+  if (!rows_ok(qr, 2) || !rows_ok(orow, 2) || (lse && !aligned(lse, 4))) return LILY_Q4_ERR_INVALID_ARG;
+  const size_t need = kv8_attention_ws_bytes(*cache, *batch, T, q_heads);
+  if (need == 0) return LILY_Q4_ERR_UNSUPPORTED;
+  if (ws_bytes < need) return LILY_Q4_ERR_WORKSPACE_TOO_SMALL;
+  const AttnShape s{T, q_heads, dtype, causal, window, scale};
+  return launch_kv8_attention(*cache, *batch, s, qr, orow, lse, ws, (cudaStream_t)stream);
 }
 
 }  // extern "C"

@@ -19,6 +19,7 @@ enum HeaderWord : int {
   kHdrCounterC = 3,
   kHdrBarrier64 = 4,  // words 4-5: 64-bit grid-barrier arrival count
   kHdrArgmax64 = 6,   // words 6-7: the LM head's running (value, row) maximum, packed (self-resetting)
+  kHdrIndexError = 12,  // nonzero after a kv8 call met a length or page number out of range
   kHdrWords = 64,
 };
 
@@ -95,6 +96,31 @@ PrefillWsLayout prefill_ws_layout(const lily_q4_moe_layer &L, int T);
 int prefill_launch_count(const lily_q4_moe_layer &L);
 int launch_moe_prefill(const lily_q4_moe_layer &L, const uint16_t *x, int T, uint16_t *y,
                        int32_t *topk_idx, float *topk_w, void *ws, cudaStream_t st);
+
+// ---------------------------------------------------------------- attention operators
+// [token][head][dim] activations with a dense last axis; strides in elements.
+struct Rows {
+  void *p;
+  int64_t ts, hs;
+};
+int rope_turns(int R, double base, int scaling, double factor, double original_len, double slow,
+               double fast, uint64_t *turns);
+int launch_qk_norm_rope(const lily_qk_rope &op, int T, int q_heads, int k_heads, const int32_t *pos,
+                        const Rows &q, const Rows &q_out, const Rows &k, const Rows &k_out,
+                        cudaStream_t st);
+int launch_kv8_append(const lily_kv8_cache &C, const lily_kv8_batch &b, int T, int dtype,
+                      const Rows &k, const Rows &v, void *ws, cudaStream_t st);
+int launch_kv8_read(const lily_kv8_cache &C, const lily_kv8_batch &b, int T, int dtype, const Rows &k,
+                    const Rows &v, void *ws, cudaStream_t st);
+struct Batch;
+Batch make_batch(const lily_kv8_cache &C, const lily_kv8_batch &b, int T);
+struct AttnShape {
+  int T, q_heads, dtype, causal, window;
+  float scale;
+};
+size_t kv8_attention_ws_bytes(const lily_kv8_cache &C, const lily_kv8_batch &b, int T, int q_heads);
+int launch_kv8_attention(const lily_kv8_cache &C, const lily_kv8_batch &b, const AttnShape &s,
+                         const Rows &q, const Rows &out, float *lse, void *ws, cudaStream_t st);
 
 int sm_count();
 int check_launch();

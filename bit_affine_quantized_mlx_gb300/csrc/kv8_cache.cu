@@ -1,0 +1,320 @@
+// The paged 8-bit key/value cache: lily_kv8_append and lily_kv8_read.
+//
+// A page and head has one magnitude amax; a code q stands for q * amax / 127.
+//
+// Append.  The new tokens of one page ("a run") are quantised with amax' = max(amax, |x|), and
+// earlier codes of the page are re-rounded when that grows.  Both roundings are those of exact
+// arithmetic, so results do not depend on how the quotient is computed: amax is always a 16-bit
+// float (8 or 11 significant bits), so 127 x and q amax are exact in fp32 (at most 18 bits).  Let
+// the numerator be an integer times 2^a and amax an integer N < 2^11 times 2^b: a quotient that is
+// not an odd multiple of 1/2 differs from every such multiple by at least 2^(a-b) / (2 N), and one
+// of 1/2 or more has 2^(a-b) >= 2^-9 or so: by 4e-7 at least.  num * (1 / den) is off by 2^-22
+// relative (2e-5 at most), so it decides everything farther than 1e-3 from a tie; nearer, an IEEE
+// division (3e-8 off at 1/2, 2^-24 relative above) decides, and gives an exact tie exactly.
+//
+// Bound by memory: 2 bytes in and 1 byte out an element; at one token a sequence by the launch
+// and one chain of dependent reads (lengths, page number, magnitude).  A run is read once, held
+// in registers between finding its magnitude and writing its codes.
+#include <algorithm>
+#include <type_traits>
+
+#include "kv8_device.cuh"
+
+namespace lq4 {
+
+struct CacheArgs {
+  Batch B;
+  int32_t *hdr;
+  int8_t *codes[2];
+  float *amax[2];
+  const void *x[2];   // append: rows in
+  void *y[2];         // read: rows out
+  int64_t ts[2], hs[2];
+  int kv_heads, D, chunk;
+};
+
+constexpr int kAppendThreads = 256;
+
+// rint(num / den) of exact arithmetic; num and den as described above, inv = 1 / den.
+__device__ __forceinline__ int exact_code(float num, float den, float inv) {
+  float q = num * inv;
+  if (!(fabsf(q - rintf(q)) < 0.499f)) q = __fdiv_rn(num, den);
+  return __float2int_rn(fminf(fmaxf(q, -127.f), 127.f));
+}
+
+__device__ __forceinline__ uint32_t umax16x2(uint32_t a, uint32_t b) { return __vmaxu2(a, b); }
+
+// TEAM threads handle a run; NV chunks of 8 elements a thread hold it (TEAM * NV * 8 >= its size).
+// TEAM = 32 (short runs: decode): a block has 8 teams, one token each.  TEAM = 256: the block
+// walks the runs that start among its `chunk` tokens.
+template <typename Ty, int TEAM, int NV>
+__global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(CacheArgs a) {
+  __shared__ uint32_t s_max[kAppendThreads / 32];
+  pdl_wait();
+  const Batch &B = a.B;
+  const int tid = threadIdx.x & (TEAM - 1), team = threadIdx.x / TEAM;
+  constexpr int TEAMS = kAppendThreads / TEAM;
+  const int h = blockIdx.y, kv = blockIdx.z;
+  const int cpr = a.D >> 3;  // chunks of 8 a row
+  const int t_first = (blockIdx.x * TEAMS + team) * a.chunk;
+  const int t_end = min(B.T, t_first + a.chunk);
+
+  for (int t = t_first; t < t_end;) {
+    const int b = find_seq(B, t);
+    const Seq s = load_seq(B, b, a.hdr);
+    if (t < s.row0 || t >= s.row0 + s.n) {  // a sequence out of bounds: no run starts here
+      ++t;
+      continue;
+    }
+    const int pos = s.len - s.n + (t - s.row0);
+    if (pos < 0 || pos >= B.table_pages * B.page) {
+      record_index_error(a.hdr);
+      ++t;
+      continue;
+    }
+    const int in_page = pos & (B.page - 1);
+    const int rows = min(B.page - in_page, s.row0 + s.n - t);
+    if (t != s.row0 && in_page != 0) {  // the middle of a run that starts earlier
+      t += rows;
+      continue;
+    }
+    const int page = load_page(B, b, pos >> B.page_shift, a.hdr);
+    const int t_run = t;
+    t += rows;
+    if (page < 0) continue;
+
+    // the run's elements and their largest magnitude (as bits: NaN > infinity > finite)
+    const uint16_t *x = static_cast<const uint16_t *>(a.x[kv]) + t_run * a.ts[kv] + h * a.hs[kv];
+    uint4 v[NV];
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = i * TEAM + tid, r = c / cpr;
+      v[i] = make_uint4(0, 0, 0, 0);
+      if (r < rows) v[i] = *reinterpret_cast<const uint4 *>(x + r * a.ts[kv] + (c - r * cpr) * 8);
+    }
+    const int64_t ph = (int64_t)page * a.kv_heads + h;
+    float *amax = a.amax[kv] + ph;
+    const float was = in_page ? *amax : 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const uint32_t m = 0x7FFF7FFFu;
+      top = umax16x2(umax16x2(top, umax16x2(v[i].x & m, v[i].y & m)), umax16x2(v[i].z & m, v[i].w & m));
+    }
+    top = max(top & 0xFFFFu, top >> 16);
+    top = __reduce_max_sync(~0u, top);
+    if (TEAM > 32) {
+      if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = top;
+      __syncthreads();
+#pragma unroll
+      for (int w = 0; w < TEAM / 32; ++w) top = max(top, s_max[w]);
+    }
+    const float fresh = Ty::to_f32x2(top).x;
+    const float now = __uint_as_float(max(__float_as_uint(fresh), __float_as_uint(was)));
+    const bool finite = now < __uint_as_float(0x7F800000u), zero = !(now > 0.f);
+    // a power of two that keeps 127 x, q amax and 1 / amax inside fp32's range (exact: whatever
+    // underflows by it has code 0)
+    const float sc = now > 0x1p60f ? 0x1p-64f : now < 0x1p-60f ? 0x1p64f : 1.f;
+    const float den = now * sc, inv = 1.f / den;
+
+    int8_t *codes = a.codes[kv] + ph * B.page * a.D;
+    if (in_page && __float_as_uint(now) != __float_as_uint(was)) {
+      // the magnitude grew: re-round the page's earlier codes, 16 at a time
+      for (int c = tid; c < in_page * (a.D >> 4); c += TEAM) {
+        uint4 w = *reinterpret_cast<uint4 *>(codes + c * 16);
+        uint32_t *u = &w.x;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          uint32_t r = 0;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float q = (float)(int8_t)(u[j] >> (8 * e));
+            const int n = finite ? exact_code(q * (was * sc), den, inv) : 0;
+            r |= (uint32_t)(uint8_t)n << (8 * e);
+          }
+          u[j] = r;
+        }
+        *reinterpret_cast<uint4 *>(codes + c * 16) = w;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = i * TEAM + tid, r = c / cpr;
+      if (r < rows) {
+        float f[8];
+        unpack8<Ty>(v[i], f);
+        uint32_t r2[2] = {0, 0};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int n = finite && !zero ? exact_code(f[e] * sc * 127.f, den, inv) : 0;
+          r2[e >> 2] |= (uint32_t)(uint8_t)n << (8 * (e & 3));
+        }
+        *reinterpret_cast<uint2 *>(codes + (int64_t)(in_page + r) * a.D + (c - r * cpr) * 8) =
+            make_uint2(r2[0], r2[1]);
+      }
+    }
+    __syncwarp();
+    if (tid == 0) *amax = now;
+    if (TEAM > 32) __syncthreads();  // s_max is written again by the next run
+  }
+}
+
+// ----------------------------------------------------------------------------- read
+// A warp takes 8 tokens: lanes 0-7 find their sequences and pages together, then the warp walks
+// the tokens' 16-code chunks.  Bound by memory (1 byte in, 2 or 4 out an element).
+constexpr int kReadThreads = 256, kReadTokens = 8;
+
+template <int DT>
+__global__ void __launch_bounds__(kReadThreads) kv8_read_kernel(CacheArgs a) {
+  pdl_wait();
+  const Batch &B = a.B;
+  const int lane = threadIdx.x & 31;
+  const int t0 = (blockIdx.x * (kReadThreads / 32) + (threadIdx.x >> 5)) * kReadTokens;
+  if (t0 >= B.T) return;
+  const int kv = blockIdx.y;
+  int page = -2, in_page = 0;  // -2: the row is not written, -1: it reads as zero
+  if (lane < kReadTokens && t0 + lane < B.T) {
+    const int t = t0 + lane, b = find_seq(B, t);
+    const Seq s = load_seq(B, b, a.hdr);
+    const int pos = s.len - s.n + (t - s.row0);
+    if (t >= s.row0 && t < s.row0 + s.n) {
+      if (pos < 0 || pos >= B.table_pages * B.page) {
+        record_index_error(a.hdr);
+      } else {
+        page = load_page(B, b, pos >> B.page_shift, a.hdr);
+        in_page = pos & (B.page - 1);
+      }
+    }
+  }
+  const int per_row = a.D >> 4, per_token = per_row * a.kv_heads;
+  const int total = min(kReadTokens, B.T - t0) * per_token;
+  const int8_t *codes = a.codes[kv];
+  const float *amax = a.amax[kv];
+  for (int c0 = 0; c0 < total; c0 += 32) {
+    const int c = c0 + lane, i = min(c / per_token, kReadTokens - 1);
+    const int p = __shfl_sync(~0u, page, i), r = __shfl_sync(~0u, in_page, i);
+    if (c >= total || p == -2) continue;
+    const int j = c - i * per_token, h = j / per_row, d = (j - h * per_row) * 16;
+    float f[16];
+    if (p < 0) {
+#pragma unroll
+      for (int e = 0; e < 16; ++e) f[e] = 0.f;
+    } else {
+      const int64_t ph = (int64_t)p * a.kv_heads + h;
+      const uint4 w = *reinterpret_cast<const uint4 *>(codes + (ph * B.page + r) * a.D + d);
+      const float s = __ldg(amax + ph);
+      const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+      for (int e = 0; e < 16; ++e) f[e] = __fdiv_rn((float)(int8_t)(u[e >> 2] >> (8 * (e & 3))) * s, 127.f);
+    }
+    const int64_t off = (int64_t)(t0 + i) * a.ts[kv] + (int64_t)h * a.hs[kv] + d;
+    if (DT == LILY_F32) {
+      float *o = static_cast<float *>(a.y[kv]) + off;
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        *reinterpret_cast<float4 *>(o + 4 * e) = make_float4(f[4 * e], f[4 * e + 1], f[4 * e + 2], f[4 * e + 3]);
+    } else {
+      uint16_t *o = static_cast<uint16_t *>(a.y[kv]) + off;
+      float lo[8], hi[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        lo[e] = f[e];
+        hi[e] = f[8 + e];
+      }
+      using Ty = typename std::conditional<DT == LILY_BF16, Bf16, F16>::type;
+      *reinterpret_cast<uint4 *>(o) = pack8<Ty>(lo);
+      *reinterpret_cast<uint4 *>(o + 8) = pack8<Ty>(hi);
+    }
+  }
+}
+
+// ----------------------------------------------------------------------------- launches
+Batch make_batch(const lily_kv8_cache &C, const lily_kv8_batch &b, int T) {
+  Batch B = {};
+  B.table = b.block_table;
+  B.q_start = b.q_start;
+  B.kv_len = b.kv_len;
+  B.table_pages = b.table_pages;
+  B.batch = b.batch;
+  B.max_q = b.max_q;
+  B.max_kv = (int)std::min<int64_t>(b.max_kv, (int64_t)b.table_pages * C.page);
+  B.T = T;
+  B.page = C.page;
+  while ((1 << B.page_shift) < C.page) ++B.page_shift;
+  B.n_pages = C.n_pages;
+  return B;
+}
+
+static CacheArgs cache_args(const lily_kv8_cache &C, const lily_kv8_batch &b, int T, void *ws) {
+  CacheArgs a = {};
+  a.B = make_batch(C, b, T);
+  a.hdr = static_cast<int32_t *>(ws);
+  a.codes[0] = C.k;
+  a.codes[1] = C.v;
+  a.amax[0] = C.k_amax;
+  a.amax[1] = C.v_amax;
+  a.kv_heads = C.kv_heads;
+  a.D = C.head_dim;
+  return a;
+}
+
+template <typename Ty>
+static cudaError_t launch_append(CacheArgs &a, cudaStream_t st) {
+  const int D = a.D, T = a.B.T;
+  const dim3 block(kAppendThreads);
+  // Runs of at most 4 * 32 chunks (one token of 256, four of 64 ...) are held by one warp, eight
+  // runs a block; with a block a run, its other seven warps would idle.
+  const int most = std::min(a.B.max_q, a.B.page);  // rows of the longest run
+  if (most * (D / 8) <= 128) {
+    a.chunk = 1;
+    const dim3 grid((T + 7) / 8, a.kv_heads, 2);
+    return launch_pdl(kv8_append_kernel<Ty, 32, 4>, grid, block, 0, st, a);
+  }
+  // Tokens of a block: about one sequence's or one page's worth, so that it walks one or two runs.
+  int chunk = 1;
+  while (chunk * 2 <= std::min(a.B.page, T / a.B.batch)) chunk *= 2;
+  a.chunk = chunk;
+  const dim3 grid((T + chunk - 1) / chunk, a.kv_heads, 2);
+  const int nv = most * (D / 8);
+  if (nv <= 256) return launch_pdl(kv8_append_kernel<Ty, 256, 1>, grid, block, 0, st, a);
+  if (nv <= 512) return launch_pdl(kv8_append_kernel<Ty, 256, 2>, grid, block, 0, st, a);
+  if (nv <= 1024) return launch_pdl(kv8_append_kernel<Ty, 256, 4>, grid, block, 0, st, a);
+  if (nv <= 2048) return launch_pdl(kv8_append_kernel<Ty, 256, 8>, grid, block, 0, st, a);
+  return launch_pdl(kv8_append_kernel<Ty, 256, 16>, grid, block, 0, st, a);
+}
+
+static int status_of(cudaError_t e) {
+  if (e == cudaSuccess) return LILY_Q4_OK;
+  cudaGetLastError();
+  return LILY_Q4_ERR_CUDA;
+}
+
+int launch_kv8_append(const lily_kv8_cache &C, const lily_kv8_batch &b, int T, int dtype,
+                      const Rows &k, const Rows &v, void *ws, cudaStream_t st) {
+  CacheArgs a = cache_args(C, b, T, ws);
+  a.x[0] = k.p;
+  a.x[1] = v.p;
+  a.ts[0] = k.ts;
+  a.ts[1] = v.ts;
+  a.hs[0] = k.hs;
+  a.hs[1] = v.hs;
+  return status_of(dtype == LILY_BF16 ? launch_append<Bf16>(a, st) : launch_append<F16>(a, st));
+}
+
+int launch_kv8_read(const lily_kv8_cache &C, const lily_kv8_batch &b, int T, int dtype, const Rows &k,
+                    const Rows &v, void *ws, cudaStream_t st) {
+  CacheArgs a = cache_args(C, b, T, ws);
+  a.y[0] = k.p;
+  a.y[1] = v.p;
+  a.ts[0] = k.ts;
+  a.ts[1] = v.ts;
+  a.hs[0] = k.hs;
+  a.hs[1] = v.hs;
+  const int per = kReadThreads / 32 * kReadTokens;
+  const dim3 grid((T + per - 1) / per, 2), block(kReadThreads);
+  if (dtype == LILY_BF16) return status_of(launch_pdl(kv8_read_kernel<LILY_BF16>, grid, block, 0, st, a));
+  if (dtype == LILY_F16) return status_of(launch_pdl(kv8_read_kernel<LILY_F16>, grid, block, 0, st, a));
+  return status_of(launch_pdl(kv8_read_kernel<LILY_F32>, grid, block, 0, st, a));
+}
+
+}  // namespace lq4

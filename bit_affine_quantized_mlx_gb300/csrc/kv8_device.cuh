@@ -1,0 +1,105 @@
+// Device helpers shared by the attention operators: 16-bit types, ragged batches, pages.
+#pragma once
+#include <cstdint>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "internal.h"
+
+namespace lq4 {
+
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// ----------------------------------------------------------------------------- 16-bit types
+struct Bf16 {
+  static __device__ __forceinline__ float2 to_f32x2(uint32_t v) {
+    return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u));
+  }
+  static __device__ __forceinline__ uint32_t from_f32x2(float lo, float hi) {
+    __nv_bfloat162 r = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<uint32_t *>(&r);
+  }
+};
+struct F16 {
+  static __device__ __forceinline__ float2 to_f32x2(uint32_t v) {
+    return __half22float2(*reinterpret_cast<__half2 *>(&v));
+  }
+  static __device__ __forceinline__ uint32_t from_f32x2(float lo, float hi) {
+    __half2 r = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<uint32_t *>(&r);
+  }
+};
+
+template <typename T>
+__device__ __forceinline__ void unpack8(const uint4 &v, float (&f)[8]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 p = T::to_f32x2(w[i]);
+    f[2 * i] = p.x;
+    f[2 * i + 1] = p.y;
+  }
+}
+template <typename T>
+__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
+  return make_uint4(T::from_f32x2(f[0], f[1]), T::from_f32x2(f[2], f[3]), T::from_f32x2(f[4], f[5]),
+                    T::from_f32x2(f[6], f[7]));
+}
+
+// ----------------------------------------------------------------------------- ragged batches
+struct Batch {
+  const int32_t *table, *q_start, *kv_len;
+  int table_pages, batch, max_q, max_kv, T;
+  int page, page_shift, n_pages;
+};
+
+struct Seq {
+  int row0, n, len;  // first row, rows, cached tokens (the rows' own included); n = 0: nothing to do
+};
+
+__device__ __forceinline__ void record_index_error(int32_t *hdr) { hdr[kHdrIndexError] = 1; }
+
+// Lengths and row range of sequence b; one that is out of bounds has no rows and is recorded.
+__device__ __forceinline__ Seq load_seq(const Batch &B, int b, int32_t *hdr) {
+  const int r0 = __ldg(B.q_start + b), r1 = __ldg(B.q_start + b + 1), len = __ldg(B.kv_len + b);
+  Seq s{r0, r1 - r0, len};
+  if (r0 < 0 || r1 < r0 || r1 > B.T || r1 - r0 > B.max_q || len < 0 || len > B.max_kv) {
+    record_index_error(hdr);
+    s = Seq{0, 0, 0};
+  }
+  return s;
+}
+
+// The sequence whose row range holds row t (the last one that starts at or before t and is not
+// empty); the caller checks that it does.
+__device__ __forceinline__ int find_seq(const Batch &B, int t) {
+  int lo = 0, hi = B.batch - 1;  // smallest b with q_start[b + 1] > t
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (__ldg(B.q_start + mid + 1) > t) hi = mid;
+    else lo = mid + 1;
+  }
+  return lo;
+}
+
+// Page number of entry i of sequence b, or -1 (recorded) when it names no page of the cache.
+__device__ __forceinline__ int load_page(const Batch &B, int b, int i, int32_t *hdr) {
+  const int p = __ldg(B.table + (int64_t)b * B.table_pages + i);
+  if (p < 0 || p >= B.n_pages) {
+    record_index_error(hdr);
+    return -1;
+  }
+  return p;
+}
+
+// Two 8-bit codes of a word whose sign bits are flipped (u = q + 128), as halves: 0x6400 + u is
+// the half 1024 + u, and subtracting 1152 leaves q, both exact.
+__device__ __forceinline__ uint32_t codes_f16(uint32_t u, uint32_t pick) {
+  uint32_t r = __byte_perm(u, 0x64646464u, pick);
+  const uint32_t off = 0x64806480u;
+  __half2 h = __hsub2(*reinterpret_cast<__half2 *>(&r), *reinterpret_cast<const __half2 *>(&off));
+  return *reinterpret_cast<uint32_t *>(&h);
+}
+constexpr uint32_t kPickLo = 0x4140, kPickHi = 0x4342;  // bytes 0, 1 and bytes 2, 3
+
+}  // namespace lq4

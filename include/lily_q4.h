@@ -63,6 +63,7 @@ typedef struct CUstream_st *lily_q4_stream_t;
 #define LILY_Q4_ERR_WORKSPACE_TOO_SMALL (-3)
 #define LILY_Q4_ERR_CUDA (-4)                 /* a CUDA launch or query failed */
 #define LILY_Q4_ERR_TIMEOUT (-5)              /* a bounded device-side wait gave up */
+#define LILY_Q4_ERR_INDEX (-6)                /* a length or page number on the device was out of range */
 
 #define LILY_Q4_GROUP 64
 
@@ -249,7 +250,8 @@ LILY_Q4_API int lily_q4_workspace_init(void *ws, size_t ws_bytes, lily_q4_stream
 
 /* Synchronises `stream`, then reads and clears the workspace's device-side error
  * word: LILY_Q4_OK, or LILY_Q4_ERR_TIMEOUT if a bounded wait gave up since the
- * last check. */
+ * last check, or LILY_Q4_ERR_INDEX if one of the lily_kv8_* calls met a length or a page
+ * number out of range (a time-out is reported before it). */
 LILY_Q4_API int lily_q4_workspace_status(void *ws, lily_q4_stream_t stream);
 
 /*
@@ -266,6 +268,161 @@ LILY_Q4_API int lily_q4_workspace_status(void *ws, lily_q4_stream_t stream);
  */
 LILY_Q4_API int lily_q4_selftest_timeout(void *ws, size_t ws_bytes, int32_t which,
                                          lily_q4_stream_t stream);
+
+/* ===================================================================== attention operators
+ *
+ * What runs between two MoE layers of a decode step or a prompt chunk: the norm of every
+ * query and key head with its position rotation, and grouped-query attention over a paged
+ * key/value cache held in 8 bits (the fork page, "The model", keeps attention at 8 bits).
+ *
+ * Conventions of these calls, besides those at the top of this file:
+ *  - Activations are [tokens][heads][head_dim] with the last axis dense and two strides in
+ *    ELEMENTS, so that a call takes views of a fused projection's rows: `*_ts` from one token
+ *    to the next and `*_hs` from one head to the next.  Pointers are 16-byte aligned and the
+ *    strides are multiples of 8 (of 4 for fp32).
+ *  - dtype: LILY_BF16 or LILY_F16 (and LILY_F32 where a call says so).
+ *  - No head or token count is fixed; T == 0 returns LILY_Q4_OK and enqueues nothing.
+ *  - Non-finite inputs stay where they are (a head, a page of one head, a row that reads it).
+ */
+#define LILY_BF16 0
+#define LILY_F16 1
+#define LILY_F32 2
+
+#define LILY_ROPE_NONE 0
+#define LILY_ROPE_LINEAR 1 /* every frequency divided by `factor` */
+#define LILY_ROPE_YARN 2   /* the published per-frequency ramp, see lily_rope_turns */
+
+/*
+ * lily_rope_turns -- host only: the rotation table of lily_qk_norm_rope.
+ *
+ * Pair i of R/2 turns by pos * f_i radians, f_i = base^(-2i/R).  LINEAR divides f_i by
+ * `factor`.  YARN keeps frequencies that make at least `fast` turns within `original_len`
+ * positions, divides those that make at most `slow` by `factor`, and blends linearly in the
+ * number of turns between them (its usual bounds are slow = 1, fast = 32; its attention
+ * factor 0.1 ln(factor) + 1 goes into lily_qk_rope.rope_scale).
+ * turns[i] = f_i / (2 pi) of a turn as an unsigned 64-bit fraction (2^64 = one whole turn;
+ * whole turns are dropped).  pos * turns[i] mod 2^64 is then the angle without the loss that
+ * a 32-bit product has at far positions: its error is pos * 2^-54 turns at most (the
+ * rounding of f_i in 64 bits).
+ * rotary_dim: even, 0..256.  base > 0; factor > 0; for YARN original_len > 0 and fast > slow.
+ */
+LILY_Q4_API int lily_rope_turns(int32_t rotary_dim, double base, int32_t scaling, double factor,
+                                double original_len, double slow, double fast, uint64_t *turns);
+
+/* One norm + rotation.  Host struct holding device pointers. */
+typedef struct {
+  int32_t head_dim;     /* D: a multiple of 8, 8..256 */
+  int32_t rotary_dim;   /* R: even, 0..D; the first R elements of a head are rotated */
+  int32_t interleaved;  /* 0: element i pairs with i + R/2; 1: 2i pairs with 2i + 1 */
+  int32_t dtype;        /* LILY_BF16 or LILY_F16: activations and weights */
+  int32_t normalize;    /* 0: rotation only (weights unused); 1: root-mean-square norm first */
+  float eps;            /* added to the mean square */
+  float weight_offset;  /* added to the weights (1 where a checkpoint stores w - 1) */
+  float rope_scale;     /* multiplies cos and sin */
+  const void *q_weight; /* [D], or NULL for ones */
+  const void *k_weight;
+  const uint64_t *turns; /* [R/2] from lily_rope_turns, on the device; NULL when R == 0 */
+} lily_qk_rope;
+
+/*
+ * lily_qk_norm_rope -- for every head of q and k:
+ *   y = x / sqrt(mean(x^2) + eps) * (w + weight_offset)                    (if normalize)
+ *   (y_a, y_b) <- rope_scale * (y_a cos - y_b sin, y_a sin + y_b cos), angle pos[t] * f_i
+ * in fp32, rounded once on the way out.  Elements beyond R pass through.
+ * pos: int32 [T], any value.  q_out/k_out may be the inputs themselves with the same strides.
+ * q_heads or k_heads may be 0 (its pointers are then unused).
+ */
+LILY_Q4_API int lily_qk_norm_rope(const lily_qk_rope *op, int32_t T, int32_t q_heads,
+                                  int32_t k_heads, const int32_t *pos, const void *q, int64_t q_ts,
+                                  int64_t q_hs, void *q_out, int64_t qo_ts, int64_t qo_hs,
+                                  const void *k, int64_t k_ts, int64_t k_hs, void *k_out,
+                                  int64_t ko_ts, int64_t ko_hs, lily_q4_stream_t stream);
+
+/* A paged 8-bit key/value cache.  A page holds `page` consecutive tokens of one sequence for
+ * every key/value head; each page and head has one magnitude for its keys and one for its
+ * values, and a code q in -127..127 stands for q * amax / 127.  Host struct, device pointers;
+ * codes 16-byte aligned. */
+typedef struct {
+  int8_t *k, *v;          /* [n_pages][kv_heads][page][head_dim] */
+  float *k_amax, *v_amax; /* [n_pages][kv_heads], finite and not negative */
+  int32_t n_pages;
+  int32_t kv_heads;
+  int32_t page;     /* 16, 32, 64 or 128 */
+  int32_t head_dim; /* 64, 128 or 256 */
+} lily_kv8_cache;
+
+/* The sequences of one call.  Sequence b owns rows q_start[b] .. q_start[b+1]-1 of the
+ * activations; they are its LAST tokens, at positions kv_len[b] - n_b .. kv_len[b]-1
+ * (kv_len counts them).  Position p lives in page block_table[b][p / page].  Entries beyond a
+ * sequence's last page are not read.  max_q and max_kv are the host's upper bounds of n_b and
+ * kv_len[b]; they size the launch.
+ * A sequence whose row range or length is out of bounds (n_b > max_q, kv_len > max_kv or more
+ * than table_pages pages, rows beyond T) is skipped and a page number outside the cache is
+ * passed over (its tokens are not written, read as zero, and masked in attention); either is
+ * recorded for lily_q4_workspace_status as LILY_Q4_ERR_INDEX. */
+typedef struct {
+  const int32_t *block_table; /* [batch][table_pages] */
+  const int32_t *q_start;     /* [batch + 1] */
+  const int32_t *kv_len;      /* [batch] */
+  int32_t table_pages;
+  int32_t batch; /* 0..4096 */
+  int32_t max_q;
+  int32_t max_kv;
+} lily_kv8_batch;
+
+/*
+ * lily_kv8_append -- writes the batch's tokens (k, v [T][kv_heads][head_dim]) into the cache.
+ * For every page and head that gets tokens, over the page's earlier tokens and the new ones:
+ *   amax' = max(amax, |x|);  code(x) = rint(127 x / amax')        (ties to even)
+ *   an earlier code q becomes rint(q amax / amax') when the magnitude grew.
+ * Both roundings are those of exact arithmetic.  A page whose first token is in the call
+ * forgets what it held.  No two sequences may append to the same page in one call; pages that
+ * sequences share (a common prefix) are whole and are only read.  A non-finite x makes its page
+ * and head non-finite: amax infinite or NaN, codes 0.
+ * ws: a workspace of at least 256 bytes (its error word is used).
+ */
+LILY_Q4_API int lily_kv8_append(const lily_kv8_cache *cache, const lily_kv8_batch *batch, int32_t T,
+                                int32_t dtype, const void *k, int64_t k_ts, int64_t k_hs,
+                                const void *v, int64_t v_ts, int64_t v_hs, void *ws,
+                                size_t ws_bytes, lily_q4_stream_t stream);
+
+/*
+ * lily_kv8_read -- the values of the batch's tokens, q * amax / 127 rounded once to dtype
+ * (LILY_BF16, LILY_F16 or LILY_F32): the inverse of lily_kv8_append, for moving a prefix to
+ * another cache or checking one.
+ */
+LILY_Q4_API int lily_kv8_read(const lily_kv8_cache *cache, const lily_kv8_batch *batch, int32_t T,
+                              int32_t dtype, void *k_out, int64_t k_ts, int64_t k_hs, void *v_out,
+                              int64_t v_ts, int64_t v_hs, void *ws, size_t ws_bytes,
+                              lily_q4_stream_t stream);
+
+/*
+ * lily_kv8_attention -- attention of the batch's tokens over their sequences' cached tokens
+ * (append them first: the keys include the tokens' own).
+ *   s_j = scale * q . k_j over the visible positions j;  out = sum_j softmax(s)_j v_j;
+ *   lse = log sum_j exp(s_j)
+ * q, out: [T][q_heads][head_dim]; query head i reads key/value head i / (q_heads / kv_heads).
+ * causal = 1: a token at position p sees j <= p; 0: all kv_len positions.
+ * window > 0: it sees only j > p - window; 0: no window.
+ * A row that sees nothing (kv_len 0, positions before the first) gives out 0 and lse -inf.
+ * lse: fp32 [T][q_heads] or NULL.  Scores, statistics and sums are fp32; the products take the
+ * codes exactly (fp16 holds them) against q scaled to fp16 by a power of two for each row (exact
+ * for elements down to 2^-28 of the row's largest), and the softmax weights, times their
+ * page's value magnitude over the running maximum of that product, in fp16.
+ * Values below 1e-32 in magnitude count as that small, not as what they are.
+ * q_heads: a multiple of kv_heads, at most 128 a key/value head.
+ */
+LILY_Q4_API int lily_kv8_attention(const lily_kv8_cache *cache, const lily_kv8_batch *batch,
+                                   int32_t T, int32_t q_heads, int32_t dtype, float scale,
+                                   int32_t causal, int32_t window, const void *q, int64_t q_ts,
+                                   int64_t q_hs, void *out, int64_t o_ts, int64_t o_hs, float *lse,
+                                   void *ws, size_t ws_bytes, lily_q4_stream_t stream);
+
+/* Workspace bytes of lily_kv8_attention for this cache, batch bounds (batch, max_q, max_kv),
+ * T and q_heads; 0 when they are invalid.  It is not larger for a smaller batch, T or bound. */
+LILY_Q4_API size_t lily_kv8_attention_workspace_bytes(const lily_kv8_cache *cache,
+                                                      const lily_kv8_batch *batch, int32_t T,
+                                                      int32_t q_heads);
 
 /* Human-readable name of a status code (static string). */
 LILY_Q4_API const char *lily_q4_status_string(int status);
