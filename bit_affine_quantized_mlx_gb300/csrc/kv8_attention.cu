@@ -43,22 +43,6 @@ namespace lq4 {
 constexpr int kDecThreads = 128, kDecWarps = 4, kDecStages = 3;
 constexpr int kTurnBytes = 4096;  // of keys, and of values, a warp and turn
 
-struct DecodeArgs {
-  Batch B;
-  int32_t *hdr;
-  const int8_t *k, *v;
-  const float *k_amax, *v_amax;
-  const uint16_t *q;
-  uint16_t *out;
-  int64_t q_ts, q_hs, o_ts, o_hs;
-  float *lse;
-  int kv_heads, group, causal, window;
-  float scale2;  // scale * log2(e) / 127
-  int4 *jobs;    // [grid][2]
-  float2 *ml;    // [2 grid][rows of a tile]: running maximum and sum of a part
-  float *part;   // [2 grid][rows of a tile][D]
-};
-
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -100,7 +84,7 @@ __device__ __forceinline__ RowOf row_of(const Seq &s, int rr, int h, int group) 
 }
 
 template <int D, int NT>
-__global__ void __launch_bounds__(kDecThreads, 2) kv8_decode_kernel(DecodeArgs a, int bf16) {
+__global__ void __launch_bounds__(kDecThreads, 2) kv8_decode_kernel(AttnArgs a, int bf16) {
   constexpr int RT = 8 * NT;             // rows of a tile
   constexpr int WS = kTurnBytes / D;     // tokens of a turn
   constexpr int NG = WS / 16;            // 16-token groups of a turn
@@ -349,7 +333,7 @@ __global__ void __launch_bounds__(kDecThreads, 2) kv8_decode_kernel(DecodeArgs a
         const float ka = mt[j];
         float va = mt[NG + j];
         va = va < 1e-30f ? 1e-30f : va;
-        iv[j] = __fdividef(1.f, va);
+        iv[j] = __frcp_rn(va);
         const float lv = __log2f(va);
         const int tk = tok0 + 16 * j;
         const bool whole = ka >= 0.f && tk >= all_lo && tk + 16 <= all_hi;
@@ -491,18 +475,19 @@ __global__ void __launch_bounds__(kDecThreads, 2) kv8_decode_kernel(DecodeArgs a
 #pragma unroll
       for (int w = 0; w < kDecWarps; ++w) {
         const float mw = s_m[w * RT + r];
-        den += mw == -INFINITY ? 0.f : s_l[w * RT + r] * ex2(mw - top);
+        // without a maximum the sum is 0, or NaN for a row of NaN
+        den += s_l[w * RT + r] * (mw == -INFINITY ? 1.f : ex2(mw - top));
       }
       if (split) {
         *reinterpret_cast<float2 *>(a.part + ((int64_t)slot * RT + r) * D + d) = sum;
         if (d == 0) a.ml[slot * RT + r] = make_float2(top, den);
       } else {
-        const float f = top == -INFINITY ? 0.f : 1.f / (127.f * den);
+        const float f = den == 0.f ? 0.f : 1.f / (127.f * den);
         const uint32_t w = bf16 ? Bf16::from_f32x2(sum.x * f, sum.y * f) : F16::from_f32x2(sum.x * f, sum.y * f);
         *reinterpret_cast<uint32_t *>(a.out + (int64_t)ro.row * a.o_ts + (int64_t)ro.head * a.o_hs + d) = w;
         if (d == 0 && a.lse)
           a.lse[(int64_t)ro.row * a.kv_heads * a.group + ro.head] =
-              top == -INFINITY ? -INFINITY : (top + log2f(den)) * 0.69314718056f;
+              den == 0.f ? -INFINITY : (top + log2f(den)) * 0.69314718056f;
       }
     }
     if (split && t0 == 0 && tid == 0) {
@@ -523,7 +508,7 @@ __global__ void __launch_bounds__(kDecThreads, 2) kv8_decode_kernel(DecodeArgs a
 constexpr int kJoinThreads = 256, kJoinParts = 1024;
 
 template <int D>
-__global__ void __launch_bounds__(kJoinThreads) kv8_join_kernel(DecodeArgs a, int RT, int bf16) {
+__global__ void __launch_bounds__(kJoinThreads) kv8_join_kernel(AttnArgs a, int RT, int bf16) {
   __shared__ float s_w[kJoinParts], s_red[kJoinThreads / 32], s_o[kJoinThreads * 4];
   pdl_wait();
   const int c = blockIdx.x, r = blockIdx.y, tid = threadIdx.x, lane = tid & 31;
@@ -549,7 +534,7 @@ __global__ void __launch_bounds__(kJoinThreads) kv8_join_kernel(DecodeArgs a, in
   for (int w = 0; w < kJoinThreads / 32; ++w) top = fmaxf(top, s_red[w]);
   float den = 0.f;
   for (int i = tid; i < parts; i += kJoinThreads) {
-    const float m = s_w[i], f = m == -INFINITY ? 0.f : ex2(m - top);
+    const float m = s_w[i], f = m == -INFINITY ? 1.f : ex2(m - top);  // sum and output 0, or NaN
     s_w[i] = f;
     den += f * a.ml[(int64_t)slot(i) * RT + r].y;
   }
@@ -584,14 +569,14 @@ __global__ void __launch_bounds__(kJoinThreads) kv8_join_kernel(DecodeArgs a, in
       acc.z += u.z;
       acc.w += u.w;
     }
-    const float f = top == -INFINITY ? 0.f : 1.f / (127.f * den);
+    const float f = den == 0.f ? 0.f : 1.f / (127.f * den);
     uint2 w;
     w.x = bf16 ? Bf16::from_f32x2(acc.x * f, acc.y * f) : F16::from_f32x2(acc.x * f, acc.y * f);
     w.y = bf16 ? Bf16::from_f32x2(acc.z * f, acc.w * f) : F16::from_f32x2(acc.z * f, acc.w * f);
     *reinterpret_cast<uint2 *>(a.out + (int64_t)ro.row * a.o_ts + (int64_t)ro.head * a.o_hs + col * 4) = w;
     if (col == 0 && a.lse)
       a.lse[(int64_t)ro.row * a.kv_heads * a.group + ro.head] =
-          top == -INFINITY ? -INFINITY : (top + log2f(den)) * 0.69314718056f;
+          den == 0.f ? -INFINITY : (top + log2f(den)) * 0.69314718056f;
   }
 }
 
@@ -629,7 +614,7 @@ static DecodePlan decode_plan(const lily_kv8_cache &C, const lily_kv8_batch &b, 
 }
 
 template <int D, int NT>
-static cudaError_t launch_decode_shape(const DecodeArgs &a, const DecodePlan &p, int bf16, cudaStream_t st) {
+static cudaError_t launch_decode_shape(const AttnArgs &a, const DecodePlan &p, int bf16, cudaStream_t st) {
   auto kernel = kv8_decode_kernel<D, NT>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)p.smem);
   if (e != cudaSuccess) return e;
@@ -639,22 +624,27 @@ static cudaError_t launch_decode_shape(const DecodeArgs &a, const DecodePlan &p,
 }
 
 template <int D>
-static cudaError_t launch_decode_dim(const DecodeArgs &a, const DecodePlan &p, int bf16, cudaStream_t st) {
+static cudaError_t launch_decode_dim(const AttnArgs &a, const DecodePlan &p, int bf16, cudaStream_t st) {
   if (p.nt == 1) return launch_decode_shape<D, 1>(a, p, bf16, st);
   if (p.nt == 2) return launch_decode_shape<D, 2>(a, p, bf16, st);
   if constexpr (D <= 128) return launch_decode_shape<D, 4>(a, p, bf16, st);
   return cudaErrorInvalidValue;
 }
 
+// Rows of a sequence and key/value head from which the tcgen05 form runs.
+constexpr int kPromptRows = 33;
+static bool prompt_form(const lily_kv8_cache &C, const lily_kv8_batch &b, int q_heads) {
+  return (int64_t)b.max_q * (q_heads / C.kv_heads) >= kPromptRows;
+}
+
 size_t kv8_attention_ws_bytes(const lily_kv8_cache &C, const lily_kv8_batch &b, int T, int q_heads) {
-  return decode_plan(C, b, T, q_heads).total;
+  return prompt_form(C, b, q_heads) ? prompt_plan(C, b, T, q_heads).total : decode_plan(C, b, T, q_heads).total;
 }
 
 int launch_kv8_attention(const lily_kv8_cache &C, const lily_kv8_batch &b, const AttnShape &s,
                          const Rows &q, const Rows &out, float *lse, void *ws, cudaStream_t st) {
-  const DecodePlan p = decode_plan(C, b, s.T, s.q_heads);
   uint8_t *w = static_cast<uint8_t *>(ws);
-  DecodeArgs a = {};
+  AttnArgs a = {};
   a.B = make_batch(C, b, s.T);
   a.hdr = static_cast<int32_t *>(ws);
   a.k = C.k;
@@ -673,11 +663,18 @@ int launch_kv8_attention(const lily_kv8_cache &C, const lily_kv8_batch &b, const
   a.causal = s.causal;
   a.window = s.window;
   a.scale2 = s.scale * 1.4426950408889634f / 127.f;
+  const int bf16 = s.dtype == LILY_BF16;
+  cudaError_t e;
+  if (prompt_form(C, b, s.q_heads)) {
+    e = launch_prompt(a, prompt_plan(C, b, s.T, s.q_heads), C.head_dim, bf16, w, st);
+    if (e == cudaSuccess) return LILY_Q4_OK;
+    cudaGetLastError();
+    return LILY_Q4_ERR_CUDA;
+  }
+  const DecodePlan p = decode_plan(C, b, s.T, s.q_heads);
   a.jobs = reinterpret_cast<int4 *>(w + p.off_jobs);
   a.ml = reinterpret_cast<float2 *>(w + p.off_ml);
   a.part = reinterpret_cast<float *>(w + p.off_part);
-  const int bf16 = s.dtype == LILY_BF16;
-  cudaError_t e;
   if (C.head_dim == 64) e = launch_decode_dim<64>(a, p, bf16, st);
   else if (C.head_dim == 128) e = launch_decode_dim<128>(a, p, bf16, st);
   else e = launch_decode_dim<256>(a, p, bf16, st);

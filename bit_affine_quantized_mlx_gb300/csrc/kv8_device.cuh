@@ -92,6 +92,31 @@ __device__ __forceinline__ int load_page(const Batch &B, int b, int i, int32_t *
   return p;
 }
 
+// Arguments of both forms of lily_kv8_attention.
+struct AttnArgs {
+  Batch B;
+  int32_t *hdr;
+  const int8_t *k, *v;
+  const float *k_amax, *v_amax;
+  const uint16_t *q;
+  uint16_t *out;
+  int64_t q_ts, q_hs, o_ts, o_hs;
+  float *lse;
+  int kv_heads, group, causal, window;
+  float scale2;  // scale * log2(e) / 127
+  int4 *jobs;    // items whose parts are joined by a second launch
+  float2 *ml;    // [parts][rows of a tile]: running maximum and sum of a part
+  float *part;   // [parts][rows of a tile][D]: unnormalised output
+};
+
+struct PromptPlan {
+  int items, splits;  // row tiles times key/value heads (a bound), parts of their keys
+  size_t off_jobs, off_ml, off_part, total;  // total 0: too many items
+};
+PromptPlan prompt_plan(const lily_kv8_cache &C, const lily_kv8_batch &b, int T, int q_heads);
+cudaError_t launch_prompt(const AttnArgs &args, const PromptPlan &p, int D, int bf16, uint8_t *ws,
+                          cudaStream_t st);
+
 // Two 8-bit codes of a word whose sign bits are flipped (u = q + 128), as halves: 0x6400 + u is
 // the half 1024 + u, and subtracting 1152 leaves q, both exact.
 __device__ __forceinline__ uint32_t codes_f16(uint32_t u, uint32_t pick) {
