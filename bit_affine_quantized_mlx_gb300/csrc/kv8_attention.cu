@@ -241,13 +241,13 @@ __global__ void __launch_bounds__(kDecThreads, 2) kv8_decode_kernel(AttnArgs a, 
     const int turns = min(t1 - t0, max(0, (hi - first + TILE - 1) / TILE));
     auto page_of = [&](int idx) {  // page of 16-token group idx of this warp's turns
       const int i = idx / NG, tok = first + i * TILE + (idx - i * NG) * 16;
-      return i < turns && tok < hi ? load_page(B, b, tok >> B.page_shift, a.hdr) : -1;
+      return i < turns && tok < hi ? raw_page(B, b, tok >> B.page_shift) : kNoPage;
     };
-    int pages = page_of(lane), pages_next = page_of(32 + lane);
+    int pages = check_page(B, page_of(lane), a.hdr), pages_next = page_of(32 + lane);
     auto issue = [&](int i) {
       const int idx = i * NG, st = i % kDecStages;
       if (i > 0 && (idx & 31) == 0) {
-        pages = pages_next;
+        pages = check_page(B, pages_next, a.hdr);
         pages_next = page_of(idx + 32 + lane);
       }
       const uint32_t dst = ring_u32 + st * 2 * kTurnBytes;

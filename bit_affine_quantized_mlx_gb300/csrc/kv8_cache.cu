@@ -78,7 +78,7 @@ __global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(CacheArgs a)
       t += rows;
       continue;
     }
-    const int page = load_page(B, b, pos >> B.page_shift, a.hdr);
+    const int page = check_page(B, raw_page(B, b, pos >> B.page_shift), a.hdr);
     const int t_run = t;
     t += rows;
     if (page < 0) continue;
@@ -181,7 +181,7 @@ __global__ void __launch_bounds__(kReadThreads) kv8_read_kernel(CacheArgs a) {
       if (pos < 0 || pos >= B.table_pages * B.page) {
         record_index_error(a.hdr);
       } else {
-        page = load_page(B, b, pos >> B.page_shift, a.hdr);
+        page = check_page(B, raw_page(B, b, pos >> B.page_shift), a.hdr);
         in_page = pos & (B.page - 1);
       }
     }

@@ -1,5 +1,6 @@
 // Device helpers shared by the attention operators: 16-bit types, ragged batches, pages.
 #pragma once
+#include <climits>
 #include <cstdint>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -82,14 +83,17 @@ __device__ __forceinline__ int find_seq(const Batch &B, int t) {
   return lo;
 }
 
-// Page number of entry i of sequence b, or -1 (recorded) when it names no page of the cache.
-__device__ __forceinline__ int load_page(const Batch &B, int b, int i, int32_t *hdr) {
-  const int p = __ldg(B.table + (int64_t)b * B.table_pages + i);
-  if (p < 0 || p >= B.n_pages) {
-    record_index_error(hdr);
-    return -1;
-  }
-  return p;
+// Page number of entry i of sequence b, as it stands: checked where it is used (check_page), so that
+// a load ahead of its use does not have to be waited for.
+__device__ __forceinline__ int raw_page(const Batch &B, int b, int i) {
+  return __ldg(B.table + (int64_t)b * B.table_pages + i);
+}
+constexpr int kNoPage = INT_MIN;  // a place without a token: nothing to record
+// The page, or -1 (recorded) when it is none of the cache's.
+__device__ __forceinline__ int check_page(const Batch &B, int p, int32_t *hdr) {
+  if (p >= 0 && p < B.n_pages) return p;
+  if (p != kNoPage) record_index_error(hdr);
+  return -1;
 }
 
 // Arguments of both forms of lily_kv8_attention.

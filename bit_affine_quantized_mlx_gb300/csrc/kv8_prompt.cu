@@ -32,14 +32,14 @@ constexpr int kRows = 128, kKeys = 128;
 
 template <int D>
 struct PromptShape {
-  static constexpr int SB = D == 256 ? 2 : 1;         // S buffers
-  static constexpr int CW = D == 256 ? 8 : 4;         // converting warps
-  static constexpr int THREADS = 32 * (4 + CW + 1);
-  static constexpr int BLOCKS = D == 256 ? 1 : 2;     // of an SM
-  static constexpr int COLS = D == 256 ? 512 : 256;   // of tensor memory
-  static constexpr int TILE = kKeys * D * 2;          // bytes of a K or V tile (Q's too)
-  static constexpr int VW = D == 64 ? 2 : 4;          // words of a token a lane holds of V
-  static constexpr int SMEM = 3 * TILE + 1024;
+  static constexpr int NQ = D == 256 ? 1 : 2;   // row tiles of a block
+  static constexpr int KB = D == 256 ? 1 : 2;   // buffers of K and of V
+  static constexpr int CW = D == 256 ? 8 : 4;   // converting warps
+  static constexpr int THREADS = 32 * (8 + CW + 1);
+  static constexpr int ROWS = kRows * NQ;
+  static constexpr int TILE = kKeys * D * 2;    // bytes of a K or V tile (and of 128 rows of Q)
+  static constexpr int VW = D == 64 ? 2 : 4;    // words of a token a lane holds of V
+  static constexpr int SMEM = (NQ + 2 * KB) * TILE + 1024;
 };
 
 __device__ __forceinline__ float ex2_approx(float x) {
@@ -66,6 +66,46 @@ __device__ __forceinline__ void tm_ld32(uint32_t addr, float (&v)[32]) {
   for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
 
+// 16 columns in two steps, for work between them; the wait passes the registers through.
+__device__ __forceinline__ void tm_ld16_start(uint32_t addr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(addr)
+      : "memory");
+}
+__device__ __forceinline__ void tm_ld16_wait(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
+                 "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]),
+                 "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+               :
+               : "memory");
+}
+// f(c, 16 columns) for each 16-column group c of a row's 128, the next group's load under way.
+template <typename F>
+__device__ __forceinline__ void for_groups(uint32_t addr, F f) {
+  uint32_t x[16], y[16];
+  tm_ld16_start(addr, x);
+#pragma unroll 1
+  for (int c = 0; c < 8; c += 2) {
+    tm_ld16_wait(x);
+    tm_ld16_start(addr + 16 * c + 16, y);
+    f(c, x);
+    tm_ld16_wait(y);
+    if (c < 6) tm_ld16_start(addr + 16 * c + 32, x);
+    f(c + 1, y);
+  }
+}
+
+__device__ __forceinline__ void tm_st8(uint32_t addr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(addr),
+               "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
 // 16 columns from registers, not waited for.
 __device__ __forceinline__ void tm_st16(uint32_t addr, const uint32_t (&r)[16]) {
   asm volatile(
@@ -90,45 +130,52 @@ __device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, volatil
 
 struct PromptItem {
   int row0, n, len;  // the sequence
-  int h, rt;         // key/value head, row tile
+  int rt;            // row tile (of ROWS)
   int lo, tiles;     // first key, key tiles
 };
 
 template <int D>
-__global__ void __launch_bounds__(PromptShape<D>::THREADS, PromptShape<D>::BLOCKS)
+__global__ void __launch_bounds__(PromptShape<D>::THREADS, 1)
     kv8_prompt_kernel(AttnArgs a, int bf16, int splits) {
   using P = PromptShape<D>;
+  constexpr int NQ = P::NQ, KB = P::KB, WARPS = P::THREADS / 32;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t s_bar[8];
+  __shared__ __align__(8) uint64_t s_bar[20];
   __shared__ uint32_t s_tmem;
-  __shared__ int s_abort, s_count[P::THREADS / 32], s_found[2];
-  __shared__ float4 s_meta[4][8];
+  __shared__ int s_abort, s_count[WARPS], s_found[2];
+  __shared__ float4 s_meta[8][8];
+  __shared__ float s_max[kRows];        // head_dim 256: the rows' running maximum
+  __shared__ float2 s_ml[2][kRows];     // head_dim 256: the two groups' maximum and sum
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t base = (tc::smem_u32(smem_raw) + 1023u) & ~1023u;
   uint8_t *const mem = smem_raw + (base - tc::smem_u32(smem_raw));
-  const uint32_t sq = base, sk = base + P::TILE, sv = base + 2 * P::TILE;
+  constexpr uint32_t kAt = NQ * P::TILE, vAt = (NQ + KB) * P::TILE;  // K and V buffers
   const uint32_t bar = tc::smem_u32(s_bar);
-  const uint32_t k_full = bar, v_full = bar + 8, pv_done = bar + 16, drain = bar + 24;
-  const uint32_t s_full = bar + 32, p_full = bar + 48;  // [SB] each
+  const uint32_t k_full = bar, v_full = bar + 16, k_free = bar + 32, v_free = bar + 48;  // [KB]
+  const uint32_t s_full = bar + 64, p_full = bar + 80, pv_done = bar + 96, m_full = bar + 112;  // [2]
+  const uint32_t drain = bar + 128;
 
   if (tid == 0) {
     s_abort = 0;
     s_found[0] = -1;
-    const int kt = D == 256 ? 128 : 32 * P::CW, vt = kt;
-    tc::mbar_init(k_full, kt);
-    tc::mbar_init(v_full, vt);
-    tc::mbar_init(pv_done, 1);
-    tc::mbar_init(drain, 1);
-    for (int i = 0; i < P::SB; ++i) {
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(k_full + 8 * i, 128);
+      tc::mbar_init(v_full + 8 * i, 128);
+      tc::mbar_init(k_free + 8 * i, 1);
+      tc::mbar_init(v_free + 8 * i, 1);
       tc::mbar_init(s_full + 8 * i, 1);
       tc::mbar_init(p_full + 8 * i, 128);
+      tc::mbar_init(pv_done + 8 * i, 1);
+      tc::mbar_init(m_full + 8 * i, 128);
     }
+    tc::mbar_init(drain, 1);
     tc::mbar_init_fence();
   }
   if (warp == 0) {
-    tc::tmem_alloc(tc::smem_u32(&s_tmem), P::COLS);
+    tc::tmem_alloc(tc::smem_u32(&s_tmem), 512);
     tc::tmem_relinquish();
   }
+  if (tid < kRows) s_max[tid] = -INFINITY;
   pdl_wait();
   const Batch &B = a.B;
   int32_t *err = a.hdr + kHdrError;
@@ -138,14 +185,14 @@ __global__ void __launch_bounds__(PromptShape<D>::THREADS, PromptShape<D>::BLOCK
   auto tiles_of = [&](int b) {
     if (b >= B.batch) return 0;
     const Seq s = load_seq(B, b, a.hdr);
-    return (s.n * a.group + kRows - 1) / kRows;
+    return (s.n * a.group + P::ROWS - 1) / P::ROWS;
   };
   int total = 0;
   for (int b0 = 0; b0 < B.batch; b0 += P::THREADS) {
     const int n = __reduce_add_sync(~0u, tiles_of(b0 + tid));
     if (lane == 0) s_count[warp] = n;
     __syncthreads();
-    for (int w = 0; w < P::THREADS / 32; ++w) total += s_count[w];
+    for (int w = 0; w < WARPS; ++w) total += s_count[w];
     __syncthreads();
   }
   const int h = blockIdx.x % a.kv_heads, want = total - 1 - (int)(blockIdx.x / a.kv_heads);
@@ -168,43 +215,48 @@ __global__ void __launch_bounds__(PromptShape<D>::THREADS, PromptShape<D>::BLOCK
         s_found[0] = b0 + tid;
         s_found[1] = want - (sum - n);
       }
-      for (int w = 0; w < P::THREADS / 32; ++w) before += s_count[w];
+      for (int w = 0; w < WARPS; ++w) before += s_count[w];
       __syncthreads();
     }
   }
   __syncthreads();
   tc::tc_fence_after();
   const uint32_t tmem = s_tmem;
-  PromptItem it = {0, 0, 0, h, 0, 0, 0};
-  if (s_found[0] >= 0) {
-    const Seq s = load_seq(B, s_found[0], a.hdr);
+  PromptItem it = {0, 0, 0, 0, 0, 0};
+  const int b_seq = s_found[0];
+  if (b_seq >= 0) {
+    const Seq s = load_seq(B, b_seq, a.hdr);
     it.row0 = s.row0;
     it.n = s.n;
     it.len = s.len;
     it.rt = s_found[1];
-    const int p_first = s.len - s.n + it.rt * kRows / a.group;
-    const int p_last = s.len - s.n + min(s.n - 1, (it.rt * kRows + kRows - 1) / a.group);
+    const int p_first = s.len - s.n + it.rt * P::ROWS / a.group;
+    const int p_last = s.len - s.n + min(s.n - 1, (it.rt * P::ROWS + P::ROWS - 1) / a.group);
     it.lo = a.window ? max(0, p_first - a.window + 1) & ~15 : 0;
     const int hi = a.causal ? min(p_last + 1, s.len) : s.len;
     it.tiles = max(0, (hi - it.lo + kKeys - 1) / kKeys);
   }
-  const int b_seq = s_found[0];
-  // this split's tiles
+  // row tiles of the block that hold rows
+  const int nq = NQ == 2 && it.n * a.group - it.rt * P::ROWS > kRows ? 2 : 1;
+  // this split's key tiles
   const int t_begin = (int)((int64_t)it.tiles * split / splits);
   const int tiles = (int)((int64_t)it.tiles * (split + 1) / splits) - t_begin;
   const int key0 = it.lo + t_begin * kKeys, len = it.len;
   const int64_t part = (int64_t)blockIdx.x * splits + split;
   if (splits > 1 && split == 0 && tid == 0)
     a.jobs[blockIdx.x] = make_int4(it.row0, it.n, h, it.rt);
-  // page of 16-key group g of this split's tile j, or -1
+  // page of 16-key group g of this split's tile j (to be checked where it is used)
   auto page_of = [&](int j, int g) {
     const int tok = key0 + j * kKeys + g * 16;
-    return j < tiles && tok < len ? load_page(B, b_seq, tok >> B.page_shift, a.hdr) : -1;
+    return j < tiles && tok < len ? raw_page(B, b_seq, tok >> B.page_shift) : kNoPage;
   };
 
-  if (warp < 4) {
+  if (warp < 8) {
     // ======================================================================== softmax
-    const int r = tid, rr = it.rt * kRows + r;
+    // Group wg of four warps: head_dim 64, 128: row tile wg, every key tile; head_dim 256: the
+    // key tiles of its parity.  Its scores are in S slot wg either way.
+    const int wg = warp >> 2, r = tid & 127;
+    const int rr = it.rt * P::ROWS + (NQ == 2 ? wg * kRows : 0) + r;
     const int tok = rr / a.group, head = h * a.group + rr - tok * a.group;
     const bool live = tok < it.n;
     const int64_t row = it.row0 + tok;
@@ -225,8 +277,10 @@ __global__ void __launch_bounds__(PromptShape<D>::THREADS, PromptShape<D>::BLOCK
       const int e = top > 0.f ? min(max(ilogbf(top), -100), 100) : 14;
       const float up = copysignf(__uint_as_float((uint32_t)(127 + 14 - e) << 23), a.scale2);
       qf = __uint_as_float((uint32_t)(127 - 14 + e) << 23) * fabsf(a.scale2);
+      uint8_t *dst = mem + (NQ == 2 ? wg * P::TILE : 0);
+      const int c0 = NQ == 2 ? 0 : wg * (D / 16), c1 = NQ == 2 ? D / 8 : c0 + D / 16;
 #pragma unroll 4
-      for (int c = 0; c < D / 8; ++c) {
+      for (int c = c0; c < c1; ++c) {
         uint4 w = make_uint4(0, 0, 0, 0);
         if (live) {
           float f[8];
@@ -236,78 +290,100 @@ __global__ void __launch_bounds__(PromptShape<D>::THREADS, PromptShape<D>::BLOCK
           for (int i = 0; i < 8; ++i) f[i] *= up;
           w = pack8<F16>(f);
         }
-        *reinterpret_cast<uint4 *>(mem + (c >> 3) * (kRows * 128) + tc::sw128(r, c & 7)) = w;
+        *reinterpret_cast<uint4 *>(dst + (c >> 3) * (kRows * 128) + tc::sw128(r, c & 7)) = w;
       }
       tc::fence_proxy_async();
     }
-    asm volatile("bar.sync 1, %0;" ::"n"(160) : "memory");  // q is there: softmax and issuing warps
+    asm volatile("bar.sync 1, 288;" ::: "memory");  // q is there: softmax and issuing warps
     // visible keys of this row, and those that every live row of the warp sees
     const int pos = it.len - it.n + tok;
     const int klo = a.window ? pos - a.window + 1 : 0, khi = a.causal ? min(pos + 1, len) : len;
     const int all_lo = __reduce_max_sync(~0u, live ? klo : INT_MIN);
     const int all_hi = __reduce_min_sync(~0u, live ? khi : INT_MAX);
-    const uint32_t t_row = tmem + ((uint32_t)(warp * 32) << 16);
-    const uint32_t t_o = t_row + 128 * P::SB;
+    const uint32_t t_row = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const uint32_t t_s = t_row + 128 * wg, t_o = t_row + 256 + (NQ == 2 ? wg * D : 0);
+    const uint32_t s_full_w = s_full + 8 * wg, p_full_w = p_full + 8 * wg;
+    const uint32_t pv_w = pv_done + (NQ == 2 ? 8 * wg : 0);
+    constexpr int STEP = NQ == 2 ? 1 : 2;
+    const int j_first = NQ == 2 ? 0 : wg, j_end = NQ == 2 && wg >= nq ? 0 : tiles;
     float m = -INFINITY, l = 0.f;
-    int page = page_of(0, lane & 7);
+    // a key tile ahead: the magnitudes of this lane's group; two ahead: its page
     auto load_mag = [&](int pg) {
-      if (pg < 0) return make_float2(-1.f, 0.f);
-      const int64_t ph = (int64_t)pg * a.kv_heads + h;
+      const int64_t ph = (int64_t)max(pg, 0) * a.kv_heads + h;
       return make_float2(__ldg(a.k_amax + ph), __ldg(a.v_amax + ph));
     };
+    int page = check_page(B, page_of(j_first, lane & 7), a.hdr);
     float2 mag = load_mag(page);
-    page = page_of(1, lane & 7);
+    int raw = page_of(j_first + STEP, lane & 7);
+    float4 *meta = s_meta[warp];
     bool ok = true;
-    for (int j = 0; j < tiles; ++j) {
+    for (int j = j_first; j < j_end; j += STEP) {
       const int k0 = key0 + j * kKeys;
-      const float va = mag.y < 1e-30f ? 1e-30f : mag.y;
-      __syncwarp();
-      if (lane < 8) s_meta[warp][lane] = make_float4(mag.x, __log2f(va), __frcp_rn(va), 0.f);
-      const bool bad = __any_sync(~0u, mag.x < 0.f);
-      const bool whole = !bad && k0 >= all_lo && k0 + kKeys <= all_hi;
+      const uint32_t turn = (NQ == 2 ? j : j >> 1) & 1;
+      const float va = page < 0 ? 1.f : mag.y < 1e-30f ? 1e-30f : mag.y;
+      const bool whole = !__any_sync(~0u, page < 0) && k0 >= all_lo && k0 + kKeys <= all_hi;
+      if (lane < 8) meta[lane] = make_float4(page < 0 ? -1.f : mag.x, __log2f(va), __frcp_rn(va), 0.f);
+      page = check_page(B, raw, a.hdr);
       mag = load_mag(page);
-      page = page_of(j + 2, lane & 7);
-      const int sb = j % P::SB;
-      ok = wait_warp(s_full + 8 * sb, (j / P::SB) & 1, abort_flag, err);
-      if (!ok) break;
+      raw = page_of(j + 2 * STEP, lane & 7);
+      __syncwarp();
+      if (!(ok = wait_warp(s_full_w, turn, abort_flag, err))) break;
       tc::tc_fence_after();
-      const uint32_t t_s = t_row + 128 * sb;
+      // A tile at the edge of what the rows see: its scores are turned into exponents here, -inf
+      // where a key is hidden, and its groups' factors become 1 (a factor of 0 would make NaN of -inf).
+      float qe = qf;
+      if (!whole) {
+#pragma unroll 1
+        for (int c = 0; c < 8; ++c) {
+          float s[16];
+          uint32_t u[16];
+          tc::tmem_ld16(t_s + 16 * c, s);
+          const float4 mt = meta[c];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const int key = k0 + 16 * c + i;
+            const float x = fmaf(s[i], mt.x * qf, mt.y);
+            u[i] = mt.x < 0.f || key < klo || key >= khi ? 0xFF800000u : __float_as_uint(x);
+          }
+          tm_st16(t_s + 16 * c, u);
+        }
+        tm_st_wait();
+        __syncwarp();
+        if (lane < 8) meta[lane].x = 1.f, meta[lane].y = 0.f;
+        __syncwarp();
+        qe = 1.f;
+      }
       // maximum: of a 16-key group's raw scores, then its factor and magnitude
       float top = -INFINITY;
+      for_groups(t_s, [&](int c, const uint32_t (&s)[16]) {
+        const float4 mt = meta[c];
+        float t = -INFINITY;
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        float s[32];
-        tm_ld32(t_s + 32 * c, s);
-#pragma unroll
-        for (int g = 0; g < 2; ++g) {
-          const float4 mt = s_meta[warp][2 * c + g];
-          float t = -INFINITY;
-          if (whole) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) t = fmaxf(t, s[16 * g + i]);
-          } else {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const int key = k0 + 32 * c + 16 * g + i;
-              if (key >= klo && key < khi && !(mt.x < 0.f)) t = fmaxf(t, s[16 * g + i]);
-            }
+        for (int i = 0; i < 16; ++i) t = fmaxf(t, __uint_as_float(s[i]));
+        if (t > -INFINITY) top = fmaxf(top, fmaf(t, mt.x * qe, mt.y));
+      });
+      // move the running maximum?  (the first tile sets it: O is not there yet)
+      if (NQ == 1) {  // the other group's last tile has decided
+        if (j > 0) {
+          if (!(ok = wait_warp(m_full + 8 * (wg ^ 1), ((j - 1) >> 1) & 1, abort_flag, err))) break;
+          const float held = s_max[r];
+          if (held != m) {
+            l *= m == -INFINITY ? 0.f : ex2_approx(m - held);
+            m = held;
           }
-          if (t > -INFINITY) top = fmaxf(top, fmaf(t, mt.x * qf, mt.y));
         }
       }
-      // move the running maximum?  (the first tile sets it: O is not there yet)
       const bool move = top > m + 8.f || (m == -INFINITY && top > m);
       if (__any_sync(~0u, move)) {
         const float now = move ? top : m;
         const float f = move ? ex2_approx(m - now) : 1.f;
         m = now;
         l *= f;
+        if (NQ == 1) s_max[r] = m;
         if (j > 0) {
-          if (P::SB > 1) {
-            ok = wait_warp(pv_done, (j - 1) & 1, abort_flag, err);
-            if (!ok) break;
-            tc::tc_fence_after();
-          }
+          // O is only touched between the product of the last tile and that of this one
+          if (!(ok = wait_warp(pv_w, (j - 1) & 1, abort_flag, err))) break;
+          tc::tc_fence_after();
 #pragma unroll 1
           for (int c = 0; c < D / 32; ++c) {
             float o[32];
@@ -323,49 +399,49 @@ __global__ void __launch_bounds__(PromptShape<D>::THREADS, PromptShape<D>::BLOCK
           }
         }
       }
+      if (NQ == 1) tc::mbar_arrive(m_full + 8 * wg);
       const float m0 = m == -INFINITY ? 0.f : m;
+      for_groups(t_s, [&](int c, const uint32_t (&s)[16]) {
+        const float4 mt = meta[c];
+        const float f = mt.x * qe, off = mt.y - m0;
+        float sum = 0.f;
+        uint32_t p[8];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        float s[32];
-        uint32_t p[16];
-        tm_ld32(t_s + 32 * c, s);
-#pragma unroll
-        for (int g = 0; g < 2; ++g) {
-          const float4 mt = s_meta[warp][2 * c + g];
-          const float f = mt.x * qf, off = mt.y - m0;
-          float sum = 0.f;
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            float x = fmaf(s[16 * g + i], f, off);
-            if (!whole) {
-              const int key = k0 + 32 * c + 16 * g + i;
-              if (key < klo || key >= khi || mt.x < 0.f) x = -INFINITY;
-            }
-            s[16 * g + i] = ex2_approx(x);
-            sum += s[16 * g + i];
-          }
-          l = fmaf(sum, mt.z, l);
-#pragma unroll
-          for (int i = 0; i < 8; ++i)
-            p[8 * g + i] = F16::from_f32x2(s[16 * g + 2 * i], s[16 * g + 2 * i + 1]);
+        for (int i = 0; i < 8; ++i) {
+          const float x0 = ex2_approx(fmaf(__uint_as_float(s[2 * i]), f, off));
+          const float x1 = ex2_approx(fmaf(__uint_as_float(s[2 * i + 1]), f, off));
+          sum += x0 + x1;
+          p[i] = F16::from_f32x2(x0, x1);
         }
-        tm_st16(t_s + 16 * c, p);
-      }
+        l = fmaf(sum, mt.z, l);
+        tm_st8(t_s + 8 * c, p);
+      });
       tm_st_wait();
       tc::tc_fence_before();
-      tc::mbar_arrive(p_full + 8 * sb);
+      tc::mbar_arrive(p_full_w);
     }
-    if (ok && tiles > 0) ok = wait_warp(pv_done, (tiles - 1) & 1, abort_flag, err);
+    if (NQ == 1) {
+      // the two groups' sums, to the common maximum
+      s_ml[wg][r] = make_float2(m, l);
+      asm volatile("bar.sync 2, 256;" ::: "memory");
+      const float2 x = s_ml[0][r], y = s_ml[1][r];
+      m = fmaxf(x.x, y.x);
+      l = x.y * (x.x == -INFINITY ? 1.f : ex2_approx(x.x - m)) + y.y * (y.x == -INFINITY ? 1.f : ex2_approx(y.x - m));
+    }
+    if (ok && j_end > 0) ok = wait_warp(pv_w, (j_end - 1) & 1, abort_flag, err);
     tc::tc_fence_after();
-    if (ok && it.n > 0) {
+    if (ok && it.n > 0 && (NQ == 1 || wg < nq)) {
       // the row saw nothing (O may not exist); a row of NaN has no maximum, but a sum of NaN
       const bool none = tiles == 0 || l == 0.f;
       if (!none && m == -INFINITY) m = 0.f;
+      const int c0 = NQ == 2 ? 0 : wg * (D / 64), c1 = NQ == 2 ? D / 32 : c0 + D / 64;
+      const bool first = NQ == 2 || wg == 0;
       if (splits > 1) {
-        float *dst = a.part + (part * kRows + r) * D;
+        const int64_t at = part * P::ROWS + (NQ == 2 ? wg * kRows : 0) + r;
+        float *dst = a.part + at * D;
         if (tiles > 0) {
 #pragma unroll 1
-          for (int c = 0; c < D / 32; ++c) {
+          for (int c = c0; c < c1; ++c) {
             float o[32];
             tm_ld32(t_o + 32 * c, o);
 #pragma unroll
@@ -374,12 +450,12 @@ __global__ void __launch_bounds__(PromptShape<D>::THREADS, PromptShape<D>::BLOCK
                   make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
           }
         }
-        a.ml[part * kRows + r] = make_float2(none ? -INFINITY : m, none ? 0.f : l);
+        if (first) a.ml[at] = make_float2(none ? -INFINITY : m, none ? 0.f : l);
       } else {
         const float f = none ? 0.f : 1.f / (127.f * l);
         uint4 *dst = reinterpret_cast<uint4 *>(a.out + row * a.o_ts + (int64_t)head * a.o_hs);
 #pragma unroll 1
-        for (int c = 0; c < D / 32; ++c) {
+        for (int c = c0; c < c1; ++c) {
           float o[32];
           if (tiles > 0) tm_ld32(t_o + 32 * c, o);
 #pragma unroll
@@ -390,150 +466,217 @@ __global__ void __launch_bounds__(PromptShape<D>::THREADS, PromptShape<D>::BLOCK
             if (live) dst[4 * c + i] = bf16 ? pack8<Bf16>(e) : pack8<F16>(e);
           }
         }
-        if (a.lse && live)
+        if (a.lse && live && first)
           a.lse[row * a.kv_heads * a.group + head] =
               none ? -INFINITY : (m + log2f(l)) * 0.69314718056f;
       }
     }
     tc::tc_fence_before();
-  } else if (warp < 4 + P::CW) {
+  } else if (warp < 8 + P::CW) {
     // ======================================================================== codes -> operands
-    constexpr bool BOTH = P::CW == 4;
-    const int w = (warp - 4) & 3;
-    const bool do_k = BOTH || warp < 8, do_v = BOTH || warp >= 8;
+    const int w = warp & 3;
     // K: this warp's 32 keys; a load covers 512 bytes of consecutive codes
     constexpr int LPR = D / 16, RPL = 32 / LPR, KL = 32 / RPL;  // lanes a row, rows a load, loads
     // V: 64 keys by 16 VW elements a unit; lane (tg, dg) holds 8 tokens' VW words
-    constexpr int VU = D / (16 * P::VW) * 2 / 4;                 // units a warp
+    constexpr int VU = D / (16 * P::VW) * 2 / 4;  // units a warp
     const int tg = lane & 7, dg = lane >> 3;
-    uint4 kr[BOTH || D == 256 ? KL : 1];
-    uint32_t vr[VU][8][P::VW];
-    int page = page_of(0, lane & 7);
-    auto load_k = [&](int j, int pages) {
+    // A page's codes beyond the sequence's end are loaded as they are, and page 0 in the place of one
+    // that is not there: their scores are hidden, so their weights are 0.  Nothing is selected after
+    // a load, which would wait for it.
+    auto load_k = [&](uint4 (&kr)[KL], int j, int raw) {
+      const int pages = check_page(B, raw, a.hdr);
 #pragma unroll
-      for (int i = 0; i < KL; ++i) {
-        const int row = i * RPL + lane / LPR, key = key0 + j * kKeys + 32 * w + row;
-        const int pg = __shfl_sync(~0u, pages, 2 * w + (i * RPL >> 4));
-        kr[i] = make_uint4(0, 0, 0, 0);
-        if (pg >= 0 && key < len)
-          kr[i] = __ldg(reinterpret_cast<const uint4 *>(
-              a.k + (((int64_t)pg * a.kv_heads + h) * B.page + (key & (B.page - 1))) * D + (lane % LPR) * 16));
+      for (int g = 0; g < 2; ++g) {
+        const int pg = max(__shfl_sync(~0u, pages, 2 * w + g), 0);
+        const int in_page = (key0 + j * kKeys + 32 * w + 16 * g) & (B.page - 1);
+        const uint4 *src = reinterpret_cast<const uint4 *>(
+            a.k + (((int64_t)pg * a.kv_heads + h) * B.page + in_page) * D) + lane;
+#pragma unroll
+        for (int i = 0; i < KL / 2; ++i) kr[g * (KL / 2) + i] = __ldg(src + i * 32);
       }
     };
-    auto load_v = [&](int j, int pages) {
+    auto store_k = [&](const uint4 (&kr)[KL], int j) {
+#pragma unroll
+      for (int i = 0; i < KL; ++i) {
+        const int row = 32 * w + i * RPL + lane / LPR, mch = lane % LPR;
+        const uint32_t u[4] = {kr[i].x ^ 0x80808080u, kr[i].y ^ 0x80808080u, kr[i].z ^ 0x80808080u,
+                               kr[i].w ^ 0x80808080u};
+        const uint4 lo = make_uint4(codes_f16(u[0], kPickLo), codes_f16(u[0], kPickHi),
+                                    codes_f16(u[1], kPickLo), codes_f16(u[1], kPickHi));
+        const uint4 hi = make_uint4(codes_f16(u[2], kPickLo), codes_f16(u[2], kPickHi),
+                                    codes_f16(u[3], kPickLo), codes_f16(u[3], kPickHi));
+        // 8 lanes of a row: the second atom's four store their odd chunk first, so that the
+        // eight 16-byte stores of a phase meet eight bank groups
+        const bool odd = (mch >> 2) & 1;
+        uint8_t *atom = mem + kAt + (j % KB) * P::TILE + (mch >> 2) * (kKeys * 128);
+        const int c = 2 * (mch & 3);
+        *reinterpret_cast<uint4 *>(atom + tc::sw128(row, c + odd)) = odd ? hi : lo;
+        *reinterpret_cast<uint4 *>(atom + tc::sw128(row, c + !odd)) = odd ? lo : hi;
+      }
+    };
+    auto load_v = [&](uint32_t (&vr)[VU][8][P::VW], int j, int raw) {
+      const int pages = check_page(B, raw, a.hdr);
 #pragma unroll
       for (int u = 0; u < VU; ++u) {
         const int unit = w * VU + u, half = unit & 1, d0 = (unit >> 1) * 16 * P::VW + dg * 4 * P::VW;
-        const int pg = __shfl_sync(~0u, pages, half * 4 + (tg >> 1));
-        const int first = key0 + j * kKeys + half * 64 + tg * 8;
-        const int8_t *src = a.v + (((int64_t)max(pg, 0) * a.kv_heads + h) * B.page + (first & (B.page - 1))) * D + d0;
+        const int pg = max(__shfl_sync(~0u, pages, half * 4 + (tg >> 1)), 0);
+        const int in_page = (key0 + j * kKeys + half * 64 + tg * 8) & (B.page - 1);
+        const int8_t *src = a.v + (((int64_t)pg * a.kv_heads + h) * B.page + in_page) * D + d0;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const bool in = pg >= 0 && first + i < len;
           if (P::VW == 4) {
-            uint4 x = make_uint4(0, 0, 0, 0);
-            if (in) x = __ldg(reinterpret_cast<const uint4 *>(src + i * D));
+            const uint4 x = __ldg(reinterpret_cast<const uint4 *>(src + i * D));
             vr[u][i][0] = x.x, vr[u][i][1] = x.y, vr[u][i][P::VW - 2] = x.z, vr[u][i][P::VW - 1] = x.w;
           } else {
-            uint2 x = make_uint2(0, 0);
-            if (in) x = __ldg(reinterpret_cast<const uint2 *>(src + i * D));
+            const uint2 x = __ldg(reinterpret_cast<const uint2 *>(src + i * D));
             vr[u][i][0] = x.x, vr[u][i][1] = x.y;
           }
         }
       }
     };
-    if (do_k) load_k(0, page);
-    if (do_v) load_v(0, page);
-    page = page_of(1, lane & 7);
-    for (int j = 0; j < tiles; ++j) {
-      if (do_k) {
-        if (j > 0 && !wait_warp(s_full + 8 * ((j - 1) % P::SB), ((j - 1) / P::SB) & 1, abort_flag, err))
-          break;
+    auto store_v = [&](const uint32_t (&vr)[VU][8][P::VW], int j) {
 #pragma unroll
-        for (int i = 0; i < KL; ++i) {
-          const int row = 32 * w + i * RPL + lane / LPR, mch = lane % LPR;
-          const uint32_t u[4] = {kr[i].x ^ 0x80808080u, kr[i].y ^ 0x80808080u, kr[i].z ^ 0x80808080u,
-                                 kr[i].w ^ 0x80808080u};
-          const uint4 lo = make_uint4(codes_f16(u[0], kPickLo), codes_f16(u[0], kPickHi),
-                                      codes_f16(u[1], kPickLo), codes_f16(u[1], kPickHi));
-          const uint4 hi = make_uint4(codes_f16(u[2], kPickLo), codes_f16(u[2], kPickHi),
-                                      codes_f16(u[3], kPickLo), codes_f16(u[3], kPickHi));
-          // 8 lanes of a row: the second atom's four store their odd chunk first, so that the
-          // eight 16-byte stores of a phase meet eight bank groups
-          const bool odd = (mch >> 2) & 1;
-          uint8_t *atom = mem + P::TILE + (mch >> 2) * (kKeys * 128);
-          const int c = 2 * (mch & 3);
-          *reinterpret_cast<uint4 *>(atom + tc::sw128(row, c + odd)) = odd ? hi : lo;
-          *reinterpret_cast<uint4 *>(atom + tc::sw128(row, c + !odd)) = odd ? lo : hi;
-        }
-        tc::fence_proxy_async();
-        tc::mbar_arrive(k_full);
-        load_k(j + 1, page);
-      }
-      if (do_v) {
-        if (j > 0 && !wait_warp(pv_done, (j - 1) & 1, abort_flag, err)) break;
+      for (int u = 0; u < VU; ++u) {
+        const int unit = w * VU + u, half = unit & 1, d0 = (unit >> 1) * 16 * P::VW + dg * 4 * P::VW;
+        uint8_t *atom = mem + vAt + (j % KB) * P::TILE + half * (D * 128);
 #pragma unroll
-        for (int u = 0; u < VU; ++u) {
-          const int unit = w * VU + u, half = unit & 1, d0 = (unit >> 1) * 16 * P::VW + dg * 4 * P::VW;
-          uint8_t *atom = mem + 2 * P::TILE + half * (D * 128);
+        for (int k = 0; k < P::VW; ++k) {
+          uint32_t z[4][2];
 #pragma unroll
-          for (int k = 0; k < P::VW; ++k) {
-            uint32_t z[4][2];
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t x = vr[u][2 * i][k] ^ 0x80808080u, y = vr[u][2 * i + 1][k] ^ 0x80808080u;
+            z[i][0] = __byte_perm(x, y, 0x5140);
+            z[i][1] = __byte_perm(x, y, 0x7362);
+          }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const uint32_t x = vr[u][2 * i][k] ^ 0x80808080u, y = vr[u][2 * i + 1][k] ^ 0x80808080u;
-              z[i][0] = __byte_perm(x, y, 0x5140);
-              z[i][1] = __byte_perm(x, y, 0x7362);
-            }
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const uint32_t pick = e & 1 ? kPickHi : kPickLo;
-              *reinterpret_cast<uint4 *>(atom + tc::sw128(d0 + 4 * k + e, tg)) =
-                  make_uint4(codes_f16(z[0][e >> 1], pick), codes_f16(z[1][e >> 1], pick),
-                             codes_f16(z[2][e >> 1], pick), codes_f16(z[3][e >> 1], pick));
-            }
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t pick = e & 1 ? kPickHi : kPickLo;
+            *reinterpret_cast<uint4 *>(atom + tc::sw128(d0 + 4 * k + e, tg)) =
+                make_uint4(codes_f16(z[0][e >> 1], pick), codes_f16(z[1][e >> 1], pick),
+                           codes_f16(z[2][e >> 1], pick), codes_f16(z[3][e >> 1], pick));
           }
         }
-        tc::fence_proxy_async();
-        tc::mbar_arrive(v_full);
-        load_v(j + 1, page);
       }
-      page = page_of(j + 2, lane & 7);
+    };
+    // buffer j % KB is free once the product that read its last contents is done
+    auto free_wait = [&](uint32_t bars, int j) {
+      return j < KB || wait_warp(bars + 8 * (j % KB), (j / KB - 1) & 1, abort_flag, err);
+    };
+    auto publish = [&](uint32_t bars, int j) {
+      tc::fence_proxy_async();
+      tc::mbar_arrive(bars + 8 * (j % KB));
+    };
+    int page = page_of(1, lane & 7);
+    const int page0 = page_of(0, lane & 7);
+    if constexpr (P::CW == 4) {
+      uint4 kr[KL];
+      uint32_t vr[VU][8][P::VW];
+      load_k(kr, 0, page0);
+      load_v(vr, 0, page0);
+      for (int j = 0; j < tiles; ++j) {
+        const int next = page_of(j + 2, lane & 7);
+        if (!free_wait(k_free, j)) break;
+        store_k(kr, j);
+        publish(k_full, j);
+        load_k(kr, j + 1, page);
+        if (!free_wait(v_free, j)) break;
+        store_v(vr, j);
+        publish(v_full, j);
+        load_v(vr, j + 1, page);
+        page = next;
+      }
+    } else if (warp < 12) {
+      uint4 kr[KL];
+      load_k(kr, 0, page0);
+      for (int j = 0; j < tiles; ++j) {
+        const int next = page_of(j + 2, lane & 7);
+        if (!free_wait(k_free, j)) break;
+        store_k(kr, j);
+        publish(k_full, j);
+        load_k(kr, j + 1, page);
+        page = next;
+      }
+    } else {
+      uint32_t vr[VU][8][P::VW];
+      load_v(vr, 0, page0);
+      for (int j = 0; j < tiles; ++j) {
+        const int next = page_of(j + 2, lane & 7);
+        if (!free_wait(v_free, j)) break;
+        store_v(vr, j);
+        publish(v_full, j);
+        load_v(vr, j + 1, page);
+        page = next;
+      }
     }
   } else {
     // ======================================================================== products
-    asm volatile("bar.sync 1, %0;" ::"n"(160) : "memory");
-    const uint32_t t_o = tmem + 128 * P::SB;
+    asm volatile("bar.sync 1, 288;" ::: "memory");
     bool ok = true;
-    auto issue_qk = [&](int j) {
-      ok = ok && wait_warp(k_full, j & 1, abort_flag, err);
+    auto wait = [&](uint32_t b, int phase) { ok = ok && wait_warp(b, phase & 1, abort_flag, err); };
+    auto issue_qk = [&](int j, int q, int slot) {  // S slot = Q(q) K(j)^T
       if (!ok) return;
       tc::tc_fence_after();
+      const uint32_t sq = base + q * P::TILE, sk = base + kAt + (j % KB) * P::TILE;
 #pragma unroll
       for (int ks = 0; ks < D / 16; ++ks) {
         const uint32_t off = (ks >> 2) * (kKeys * 128) + (ks & 3) * 32;
-        tc::mma_bf16_warp(tmem + 128 * (j % P::SB), tc::desc_k128_sw128(sq + off),
-                          tc::desc_k128_sw128(sk + off), idesc_f16(kKeys), ks > 0);
+        tc::mma_bf16_warp(tmem + 128 * slot, tc::desc_k128_sw128(sq + off), tc::desc_k128_sw128(sk + off),
+                          idesc_f16(kKeys), ks > 0);
       }
-      tc::mma_commit_warp(s_full + 8 * (j % P::SB));
+      tc::mma_commit_warp(s_full + 8 * slot);
     };
-    if (P::SB > 1 && tiles > 0) issue_qk(0);
-    for (int j = 0; j < tiles && ok; ++j) {
-      // S(j + SB - 1) takes the columns of P(j - 1): that product has to be done
-      if (j > 0) ok = ok && wait_warp(pv_done, (j - 1) & 1, abort_flag, err);
-      if (P::SB == 1) issue_qk(j);
-      else if (j + 1 < tiles) issue_qk(j + 1);
-      ok = ok && wait_warp(v_full, j & 1, abort_flag, err);
-      ok = ok && wait_warp(p_full + 8 * (j % P::SB), (j / P::SB) & 1, abort_flag, err);
-      if (!ok) break;
+    auto issue_pv = [&](int j, int q, int slot) {  // O(q) += P slot V(j)
+      if (!ok) return;
       tc::tc_fence_after();
+      const uint32_t sv = base + vAt + (j % KB) * P::TILE;
 #pragma unroll
       for (int ks = 0; ks < kKeys / 16; ++ks) {
         const uint32_t off = (ks >> 2) * (D * 128) + (ks & 3) * 32;
-        tc::mma_bf16_ts_warp(t_o, tmem + 128 * (j % P::SB) + 8 * ks, tc::desc_k128_sw128(sv + off),
+        tc::mma_bf16_ts_warp(tmem + 256 + q * D, tmem + 128 * slot + 8 * ks, tc::desc_k128_sw128(sv + off),
                              idesc_f16(D), j > 0 || ks > 0);
       }
-      tc::mma_commit_warp(pv_done);
+      tc::mma_commit_warp(pv_done + 8 * q);
+    };
+    if (NQ == 2) {
+      // the two row tiles take turns: while one's weights are computed the other's products run
+      if (tiles > 0) {
+        wait(k_full, 0);
+        for (int q = 0; q < nq; ++q) issue_qk(0, q, q);
+        if (ok) tc::mma_commit_warp(k_free);
+      }
+      for (int j = 0; j < tiles && ok; ++j) {
+        wait(v_full + 8 * (j % KB), j / KB);
+        for (int q = 0; q < nq; ++q) {
+          wait(p_full + 8 * q, j);
+          issue_pv(j, q, q);
+          if (q == nq - 1 && ok) tc::mma_commit_warp(v_free + 8 * (j % KB));
+          if (j + 1 < tiles) {
+            if (q == 0) wait(k_full + 8 * ((j + 1) % KB), (j + 1) / KB);
+            wait(pv_done + 8 * q, j);  // S takes the columns of P
+            issue_qk(j + 1, q, q);
+            if (q == nq - 1 && ok) tc::mma_commit_warp(k_free + 8 * ((j + 1) % KB));
+          }
+        }
+      }
+    } else {
+      // the next tile's scores are computed under this one's softmax, in the other slot
+      if (tiles > 0) {
+        wait(k_full, 0);
+        issue_qk(0, 0, 0);
+        if (ok) tc::mma_commit_warp(k_free);
+      }
+      for (int j = 0; j < tiles && ok; ++j) {
+        if (j + 1 < tiles) {
+          if (j > 0) wait(pv_done, j - 1);  // that slot's weights have been used
+          wait(k_full, j + 1);
+          issue_qk(j + 1, 0, (j + 1) & 1);
+          if (ok) tc::mma_commit_warp(k_free);
+        }
+        wait(v_full, j);
+        wait(p_full + 8 * (j & 1), j >> 1);
+        issue_pv(j, 0, j & 1);
+        if (ok) tc::mma_commit_warp(v_free);
+      }
     }
     // nothing of this warp's products is in flight when the tensor memory is given back
     tc::mma_commit_warp(drain);
@@ -542,29 +685,30 @@ __global__ void __launch_bounds__(PromptShape<D>::THREADS, PromptShape<D>::BLOCK
     tc::tc_fence_before();
   }
   __syncthreads();
-  if (warp == 0) tc::tmem_dealloc(tmem, P::COLS);
+  if (warp == 0) tc::tmem_dealloc(tmem, 512);
 }
 
 // ----------------------------------------------------------------------------- join
 // A warp takes a row of a split item: the splits in order.
 template <int D>
 __global__ void __launch_bounds__(256) kv8_prompt_join_kernel(AttnArgs a, int bf16, int splits) {
+  constexpr int ROWS = PromptShape<D>::ROWS;
   pdl_wait();
   const int item = blockIdx.x, r = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   const int4 j = a.jobs[item];
-  const int rr = j.w * kRows + r, tok = rr / a.group;
+  const int rr = j.w * ROWS + r, tok = rr / a.group;
   if (tok >= j.y) return;
   const int head = j.z * a.group + rr - tok * a.group;
   const int64_t row = j.x + tok;
   float top = -INFINITY, den = 0.f;
   for (int s = 0; s < splits; ++s)
-    top = fmaxf(top, a.ml[((int64_t)item * splits + s) * kRows + r].x);
+    top = fmaxf(top, a.ml[((int64_t)item * splits + s) * ROWS + r].x);
   constexpr int E = D / 32;
   float acc[E];
 #pragma unroll
   for (int i = 0; i < E; ++i) acc[i] = 0.f;
   for (int s = 0; s < splits; ++s) {
-    const int64_t at = ((int64_t)item * splits + s) * kRows + r;
+    const int64_t at = ((int64_t)item * splits + s) * ROWS + r;
     const float2 ml = a.ml[at];
     if (ml.x == -INFINITY) continue;  // its output was not written
     const float f = ex2_approx(ml.x - top);
@@ -592,26 +736,27 @@ __global__ void __launch_bounds__(256) kv8_prompt_join_kernel(AttnArgs a, int bf
 PromptPlan prompt_plan(const lily_kv8_cache &C, const lily_kv8_batch &b, int T, int q_heads) {
   PromptPlan p = {};
   const int64_t group = q_heads / C.kv_heads, D = C.head_dim;
+  const int64_t R = kRows * (D == 256 ? 1 : 2);
   // row tiles: every sequence's last one may be partly filled
-  const int64_t rows = std::min<int64_t>(T * group / kRows + std::min(b.batch, T),
-                                         std::min<int64_t>(b.batch, T) * ((b.max_q * group + kRows - 1) / kRows));
+  const int64_t rows = std::min<int64_t>(T * group / R + std::min(b.batch, T),
+                                         std::min<int64_t>(b.batch, T) * ((b.max_q * group + R - 1) / R));
   const int64_t items = std::max<int64_t>(1, rows) * C.kv_heads;
   if (items > INT32_MAX) return p;
   const int sms = sm_count() > 0 ? sm_count() : 152;
-  const int64_t slots = sms * (D == 256 ? 1 : 2), tiles = (b.max_kv + 16LL + kKeys - 1) / kKeys;
+  const int64_t tiles = (b.max_kv + 16LL + kKeys - 1) / kKeys;
   // Few row tiles: the keys are split too, so that every SM has a share, of four tiles at least (a
   // share costs its block's start and a write and read of its output).
   p.items = (int)items;
-  p.splits = (int)std::max<int64_t>(1, std::min<int64_t>(slots / items, tiles / 4));
+  p.splits = (int)std::max<int64_t>(1, std::min<int64_t>(sms / items, tiles / 4));
   p.total = kAlign;
   if (p.splits > 1) {
     size_t off = kAlign;
     p.off_jobs = off;
     off = align_up(off + items * sizeof(int4));
     p.off_ml = off;
-    off = align_up(off + items * p.splits * kRows * sizeof(float2));
+    off = align_up(off + items * p.splits * R * sizeof(float2));
     p.off_part = off;
-    p.total = align_up(off + (size_t)items * p.splits * kRows * D * sizeof(float));
+    p.total = align_up(off + (size_t)items * p.splits * R * D * sizeof(float));
   }
   return p;
 }
@@ -623,7 +768,7 @@ static cudaError_t launch_prompt_dim(const AttnArgs &a, const PromptPlan &p, int
   if (e != cudaSuccess) return e;
   e = launch_pdl(kv8_prompt_kernel<D>, dim3(p.items, p.splits), dim3(P::THREADS), P::SMEM, st, a, bf16, p.splits);
   if (e != cudaSuccess || p.splits == 1) return e;
-  return launch_pdl(kv8_prompt_join_kernel<D>, dim3(p.items, kRows / 8), dim3(256), 0, st, a, bf16, p.splits);
+  return launch_pdl(kv8_prompt_join_kernel<D>, dim3(p.items, P::ROWS / 8), dim3(256), 0, st, a, bf16, p.splits);
 }
 
 cudaError_t launch_prompt(const AttnArgs &args, const PromptPlan &p, int D, int bf16, uint8_t *ws,
