@@ -394,14 +394,27 @@ def lily_q4_unpack(w: np.ndarray, N: int, K: int) -> np.ndarray:
 
 # --------------------------------------------------------------------------- attention operators
 
+# Filled on the first call (torch is imported lazily); looked up by name, not imported, on later ones.
+_DTYPES = {}      # torch.dtype -> code
+_raw_stream = None  # device index -> handle of its current stream
+_int32_t = _float32_t = None
+
+
+def _first_use():
+    global _raw_stream, _int32_t, _float32_t
+    torch = _torch()
+    _raw_stream = torch._C._cuda_getCurrentRawStream
+    _int32_t, _float32_t = torch.int32, torch.float32
+    _DTYPES.update({torch.bfloat16: BF16, torch.int16: BF16, torch.float16: F16, torch.float32: F32})
+
+
 def _dtype_code(t, what, f32=False):
     """bf16 tensors (or their bits as int16, as elsewhere in this binding), fp16, fp32 if allowed."""
-    name = str(t.dtype)
-    code = {"torch.bfloat16": BF16, "torch.int16": BF16, "torch.float16": F16}.get(name)
-    if code is None and f32 and name == "torch.float32":
-        code = F32
-    if code is None:
-        raise Q4Error(ERR_UNSUPPORTED, f"{what}: dtype {name}")
+    if _raw_stream is None:
+        _first_use()
+    code = _DTYPES.get(t.dtype)
+    if code is None or (code == F32 and not f32):
+        raise Q4Error(ERR_UNSUPPORTED, f"{what}: dtype {t.dtype}")
     return code
 
 
@@ -410,15 +423,19 @@ def _require(ok, what):
         raise Q4Error(ERR_INVALID_ARG, what)
 
 
-def _rows(t, heads, dim, what):
-    """(pointer, token stride, head stride) of a [T, heads, dim] tensor with a dense last axis."""
-    _require(t.dim() == 3 and t.shape[2] == dim and (heads is None or t.shape[1] == heads)
-             and (t.stride(2) == 1 or t.numel() == 0), f"{what}: shape {tuple(t.shape)}")
-    return t.data_ptr(), t.stride(0), t.stride(1)
+def _rows(t, rows, heads, dim, what):
+    """(pointer, token stride, head stride) of a [rows, heads, dim] tensor with a dense last axis."""
+    step = t.stride()
+    if t.shape != (rows, heads, dim) or (step[2] != 1 and t.numel()):
+        raise Q4Error(ERR_INVALID_ARG, f"{what}: shape {tuple(t.shape)}, strides {step}")
+    return t.data_ptr(), step[0], step[1]
 
 
 def _int32(t, what):
-    _require(str(t.dtype) == "torch.int32" and t.is_contiguous(), f"{what}: contiguous int32")
+    if _raw_stream is None:
+        _first_use()
+    if t.dtype is not _int32_t or not t.is_contiguous():
+        raise Q4Error(ERR_INVALID_ARG, f"{what}: contiguous int32")
     return t.data_ptr()
 
 
@@ -457,32 +474,37 @@ class QKNormRope:
                                self.dtype or 0, int(bool(normalize)), float(eps),
                                float(weight_offset), float(rope_scale), _ptr(q_weight),
                                _ptr(k_weight), _ptr(turns) if rotary_dim else None)
+        self._ref = C.byref(self._c)
 
-    def c(self, dtype) -> lily_qk_rope:
-        _require(self.dtype in (None, dtype), "lily_qk_norm_rope: weights and heads of two types")
+    def c(self, dtype):
+        """The C struct by reference, for heads of this type."""
+        if self.dtype not in (None, dtype):
+            raise Q4Error(ERR_INVALID_ARG, "lily_qk_norm_rope: weights and heads of two types")
         self._c.dtype = dtype
-        return self._c
+        return self._ref
 
 
 def lily_qk_norm_rope(op: QKNormRope, q, k, pos, q_out, k_out, stream=None):
     """Norm and rotation of every head of q [T, q_heads, D] and k [T, k_heads, D] (views with any
     token and head strides) into q_out and k_out, which may be q and k; k may be None."""
-    T, d = int(q.shape[0]), op.head_dim
+    T, hq, d = q.shape[0], q.shape[1], op.head_dim
     dtype = _dtype_code(q, "lily_qk_norm_rope")
-    _require(q_out.dtype == q.dtype and q_out.shape == q.shape, "lily_qk_norm_rope: q_out")
-    heads, kr, ko = 0, (None, 0, 0), (None, 0, 0)
+    if q_out.dtype != q.dtype or (k is not None and not k.dtype == k_out.dtype == q.dtype):
+        raise Q4Error(ERR_INVALID_ARG, "lily_qk_norm_rope: q, k and their outputs of one type")
+    hk, kr, ko = 0, (None, 0, 0), (None, 0, 0)
     if k is not None:
-        _require(k.dtype == q.dtype and k_out.dtype == q.dtype and k_out.shape == k.shape
-                 and k.shape[0] == T, "lily_qk_norm_rope: k, k_out")
-        heads, kr, ko = int(k.shape[1]), _rows(k, None, d, "k"), _rows(k_out, None, d, "k_out")
+        hk = k.shape[1]
+        kr, ko = _rows(k, T, hk, d, "k"), _rows(k_out, T, hk, d, "k_out")
     if op.rotary_dim:
         _require(pos.numel() == T, "lily_qk_norm_rope: pos")
         pos = _int32(pos, "pos")
     else:
         pos = None
-    return _check(load().lily_qk_norm_rope(C.byref(op.c(dtype)), T, int(q.shape[1]), heads, pos,
-                                           *_rows(q, None, d, "q"), *_rows(q_out, None, d, "q_out"),
-                                           *kr, *ko, _stream(stream)), "lily_qk_norm_rope")
+    rc = (_lib or load()).lily_qk_norm_rope(op.c(dtype), T, hq, hk, pos, *_rows(q, T, hq, d, "q"),
+                                            *_rows(q_out, T, hq, d, "q_out"), *kr, *ko,
+                                            _raw_stream(q.get_device()) if stream is None
+                                            else stream.cuda_stream)
+    return rc if rc == OK else _check(rc, "lily_qk_norm_rope")
 
 
 class KV8Cache:
@@ -499,6 +521,7 @@ class KV8Cache:
         self.n_pages, self.kv_heads, self.page, self.head_dim = (int(n) for n in k.shape)
         self._c = lily_kv8_cache(_ptr(k), _ptr(v), _ptr(k_amax), _ptr(v_amax), self.n_pages,
                                  self.kv_heads, self.page, self.head_dim)
+        self._ref = C.byref(self._c)
 
     @classmethod
     def new(cls, n_pages, kv_heads, page, head_dim, device="cuda"):
@@ -509,8 +532,9 @@ class KV8Cache:
                 for _ in range(2)]
         return cls(*codes, *amax)
 
-    def c(self) -> lily_kv8_cache:
-        return self._c
+    def c(self):
+        """The C struct by reference."""
+        return self._ref
 
 
 class KV8Batch:
@@ -525,47 +549,56 @@ class KV8Batch:
         self._c = lily_kv8_batch(_int32(block_table, "block_table"), _int32(q_start, "q_start"),
                                  _int32(kv_len, "kv_len"), int(block_table.shape[1]), n, int(max_q),
                                  int(max_kv))
+        self._ref = C.byref(self._c)
 
-    def c(self) -> lily_kv8_batch:
-        return self._c
+    def c(self):
+        """The C struct by reference."""
+        return self._ref
 
 
 def _kv8_rows(fn, name, cache, batch, k, v, ws, stream, f32):
-    T, h, d = int(k.shape[0]), cache.kv_heads, cache.head_dim
+    T, h, d = k.shape[0], cache.kv_heads, cache.head_dim
     dtype = _dtype_code(k, name, f32)
-    _require(v.dtype == k.dtype and v.shape[0] == T, f"{name}: k and v")
-    return _check(fn(C.byref(cache.c()), C.byref(batch.c()), T, dtype, *_rows(k, h, d, "k"),
-                     *_rows(v, h, d, "v"), _ptr(ws), ws.numel() if ws is not None else 0,
-                     _stream(stream)), name)
+    if v.dtype != k.dtype:
+        raise Q4Error(ERR_INVALID_ARG, f"{name}: k and v of one type")
+    rc = fn(cache.c(), batch.c(), T, dtype, *_rows(k, T, h, d, "k"), *_rows(v, T, h, d, "v"),
+            *_space(ws), _raw_stream(k.get_device()) if stream is None else stream.cuda_stream)
+    return rc if rc == OK else _check(rc, name)
+
+
+def _space(ws):
+    return (None, 0) if ws is None else (ws.data_ptr(), ws.numel() * ws.element_size())
 
 
 def lily_kv8_append(cache: KV8Cache, batch: KV8Batch, k, v, ws=None, stream=None):
     """Writes the batch's tokens k, v [T, kv_heads, head_dim] into the cache; see include/lily_q4.h."""
-    return _kv8_rows(load().lily_kv8_append, "lily_kv8_append", cache, batch, k, v, ws, stream, False)
+    return _kv8_rows((_lib or load()).lily_kv8_append, "lily_kv8_append", cache, batch, k, v, ws, stream, False)
 
 
 def lily_kv8_read(cache: KV8Cache, batch: KV8Batch, k_out, v_out, ws=None, stream=None):
     """The values of the batch's tokens into k_out, v_out (bf16, fp16 or fp32)."""
-    return _kv8_rows(load().lily_kv8_read, "lily_kv8_read", cache, batch, k_out, v_out, ws, stream, True)
+    return _kv8_rows((_lib or load()).lily_kv8_read, "lily_kv8_read", cache, batch, k_out, v_out, ws, stream, True)
 
 
 def lily_kv8_attention_workspace_bytes(cache: KV8Cache, batch: KV8Batch, T: int, q_heads: int) -> int:
-    return int(load().lily_kv8_attention_workspace_bytes(C.byref(cache.c()), C.byref(batch.c()),
-                                                         int(T), int(q_heads)))
+    return int(load().lily_kv8_attention_workspace_bytes(cache.c(), batch.c(), int(T), int(q_heads)))
 
 
 def lily_kv8_attention(cache: KV8Cache, batch: KV8Batch, q, out, scale, lse=None, causal=True,
                        window=0, ws=None, stream=None):
     """Attention of q [T, q_heads, head_dim] over the batch's cached tokens into out (same shape)
     and, if given, lse fp32 [T, q_heads]; see include/lily_q4.h."""
-    T, heads, d = int(q.shape[0]), int(q.shape[1]), cache.head_dim
+    T, heads, d = q.shape[0], q.shape[1], cache.head_dim
     dtype = _dtype_code(q, "lily_kv8_attention")
-    _require(out.dtype == q.dtype and out.shape == q.shape, "lily_kv8_attention: out")
+    if out.dtype != q.dtype:
+        raise Q4Error(ERR_INVALID_ARG, "lily_kv8_attention: q and out of one type")
     if lse is not None:
-        _require(lse.numel() == T * heads and str(lse.dtype) == "torch.float32"
-                 and lse.is_contiguous(), "lily_kv8_attention: lse is fp32 [T, q_heads]")
-    return _check(load().lily_kv8_attention(C.byref(cache.c()), C.byref(batch.c()), T, heads, dtype,
-                                            float(scale), int(bool(causal)), int(window),
-                                            *_rows(q, heads, d, "q"), *_rows(out, heads, d, "out"),
-                                            _ptr(lse), _ptr(ws), ws.numel() if ws is not None else 0,
-                                            _stream(stream)), "lily_kv8_attention")
+        if lse.shape != (T, heads) or lse.dtype is not _float32_t or not lse.is_contiguous():
+            raise Q4Error(ERR_INVALID_ARG, "lily_kv8_attention: lse is fp32 [T, q_heads]")
+        lse = lse.data_ptr()
+    rc = (_lib or load()).lily_kv8_attention(cache.c(), batch.c(), T, heads, dtype, scale,
+                                             1 if causal else 0, window, *_rows(q, T, heads, d, "q"),
+                                             *_rows(out, T, heads, d, "out"), lse, *_space(ws),
+                                             _raw_stream(q.get_device()) if stream is None
+                                             else stream.cuda_stream)
+    return rc if rc == OK else _check(rc, "lily_kv8_attention")

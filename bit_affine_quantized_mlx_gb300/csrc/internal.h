@@ -144,4 +144,16 @@ inline cudaError_t launch_pdl(void (*fn)(KArgs...), dim3 grid, dim3 block, size_
   return cudaLaunchKernelEx(&cfg, fn, args...);
 }
 
+// Opt a kernel in to `bytes` of dynamic shared memory, once a device (allowed[] is the kernel's).
+template <typename F>
+inline cudaError_t allow_smem(F *fn, size_t bytes, size_t (&allowed)[64]) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 0 && dev < 64 && allowed[dev] >= bytes) return cudaSuccess;
+  e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (e == cudaSuccess && dev >= 0 && dev < 64) allowed[dev] = bytes;
+  return e;
+}
+
 }  // namespace lq4

@@ -167,6 +167,53 @@ __global__ void __launch_bounds__(kDecThreads, 2) kv8_decode_kernel(AttnArgs a, 
     const int t1 = min(ntile, t0 + end - cur);
     const int h = item % a.kv_heads, rt = item / a.kv_heads;
 
+    // ---- this warp's turns, the first of them under way before q is read: turn i holds tokens first + i * TILE ...
+    const int first = lo + (t0 * kDecWarps + warp) * WS;
+    const int turns = min(t1 - t0, max(0, (hi - first + TILE - 1) / TILE));
+    auto page_of = [&](int idx) {  // page of 16-token group idx of this warp's turns
+      const int i = idx / NG, tok = first + i * TILE + (idx - i * NG) * 16;
+      return i < turns && tok < hi ? raw_page(B, b, tok >> B.page_shift) : kNoPage;
+    };
+    int pages = check_page(B, page_of(lane), a.hdr), pages_next = page_of(32 + lane);
+    auto issue = [&](int i) {
+      const int idx = i * NG, st = i % kDecStages;
+      if (i > 0 && (idx & 31) == 0) {
+        pages = check_page(B, pages_next, a.hdr);
+        pages_next = page_of(idx + 32 + lane);
+      }
+      const uint32_t dst = ring_u32 + st * 2 * kTurnBytes;
+      const int tok0 = first + i * TILE;
+#pragma unroll
+      for (int j = 0; j < NG; ++j) {
+        const int page = __shfl_sync(~0u, pages, (idx + j) & 31);
+        const int64_t ph = (int64_t)page * a.kv_heads + h;
+        const int64_t off = page < 0 ? 0 : (ph * B.page + ((tok0 + 16 * j) & (B.page - 1))) * D + lane * 16;
+#pragma unroll
+        for (int i2 = 0; i2 < D / 32; ++i2) {
+          const int e = i2 * 32 + lane, r = e / (D / 16), c = e % (D / 16);
+          const bool ok = page >= 0 && tok0 + 16 * j + r < hi;
+          const uint32_t to = dst + turn_addr<D>(16 * j + r, c);
+          const int64_t from = ok ? off + i2 * 512 : 0;
+          tc::cp_async16(to, a.k + from, ok ? 16 : 0);
+          tc::cp_async16(to + kTurnBytes, a.v + from, ok ? 16 : 0);
+        }
+        if (lane == j) {
+          float *mp = meta + st * 2 * NG + j;
+          if (page >= 0) {
+            tc::cp_async4(tc::smem_u32(mp), a.k_amax + ph);
+            tc::cp_async4(tc::smem_u32(mp + NG), a.v_amax + ph);
+          } else {
+            mp[0] = -1.f;  // nothing of this group is seen
+            mp[NG] = 0.f;
+          }
+        }
+      }
+    };
+#pragma unroll
+    for (int i = 0; i < kDecStages - 1; ++i) {
+      if (i < turns) issue(i);
+      tc::cp_async_commit();
+    }
     // ---- q, scaled by a power of two for each row so that its largest element is in [2^14, 2^15)
     for (int r = warp; r < RT; r += kDecWarps) {
       constexpr int E = D / 32;
@@ -236,53 +283,6 @@ __global__ void __launch_bounds__(kDecThreads, 2) kv8_decode_kernel(AttnArgs a, 
       for (int i = 0; i < MT; ++i) o[i][n][0] = o[i][n][1] = o[i][n][2] = o[i][n][3] = 0.f;
     }
 
-    // ---- this warp's turns: turn i holds tokens first + i * TILE ...
-    const int first = lo + (t0 * kDecWarps + warp) * WS;
-    const int turns = min(t1 - t0, max(0, (hi - first + TILE - 1) / TILE));
-    auto page_of = [&](int idx) {  // page of 16-token group idx of this warp's turns
-      const int i = idx / NG, tok = first + i * TILE + (idx - i * NG) * 16;
-      return i < turns && tok < hi ? raw_page(B, b, tok >> B.page_shift) : kNoPage;
-    };
-    int pages = check_page(B, page_of(lane), a.hdr), pages_next = page_of(32 + lane);
-    auto issue = [&](int i) {
-      const int idx = i * NG, st = i % kDecStages;
-      if (i > 0 && (idx & 31) == 0) {
-        pages = check_page(B, pages_next, a.hdr);
-        pages_next = page_of(idx + 32 + lane);
-      }
-      const uint32_t dst = ring_u32 + st * 2 * kTurnBytes;
-      const int tok0 = first + i * TILE;
-#pragma unroll
-      for (int j = 0; j < NG; ++j) {
-        const int page = __shfl_sync(~0u, pages, (idx + j) & 31);
-        const int64_t ph = (int64_t)page * a.kv_heads + h;
-        const int64_t off = page < 0 ? 0 : (ph * B.page + ((tok0 + 16 * j) & (B.page - 1))) * D + lane * 16;
-#pragma unroll
-        for (int i2 = 0; i2 < D / 32; ++i2) {
-          const int e = i2 * 32 + lane, r = e / (D / 16), c = e % (D / 16);
-          const bool ok = page >= 0 && tok0 + 16 * j + r < hi;
-          const uint32_t to = dst + turn_addr<D>(16 * j + r, c);
-          const int64_t from = ok ? off + i2 * 512 : 0;
-          tc::cp_async16(to, a.k + from, ok ? 16 : 0);
-          tc::cp_async16(to + kTurnBytes, a.v + from, ok ? 16 : 0);
-        }
-        if (lane == j) {
-          float *mp = meta + st * 2 * NG + j;
-          if (page >= 0) {
-            tc::cp_async4(tc::smem_u32(mp), a.k_amax + ph);
-            tc::cp_async4(tc::smem_u32(mp + NG), a.v_amax + ph);
-          } else {
-            mp[0] = -1.f;  // nothing of this group is seen
-            mp[NG] = 0.f;
-          }
-        }
-      }
-    };
-#pragma unroll
-    for (int i = 0; i < kDecStages - 1; ++i) {
-      if (i < turns) issue(i);
-      tc::cp_async_commit();
-    }
     for (int i = 0; i < turns; ++i) {
       if (i + kDecStages - 1 < turns) issue(i + kDecStages - 1);
       tc::cp_async_commit();
@@ -504,12 +504,15 @@ __global__ void __launch_bounds__(kDecThreads, 2) kv8_decode_kernel(AttnArgs a, 
 
 // ----------------------------------------------------------------------------- join
 // Block (c, r): row r of the item that block c of the first launch began and did not finish.  The
-// parts' maxima and sums first, then the outputs, groups of threads taking the parts in turns.
-constexpr int kJoinThreads = 256, kJoinParts = 1024;
+// parts' maxima and sums first (a thread each), then the outputs: a quarter of a head's four-element
+// columns take the parts in turns, eight loads in flight a thread.
+constexpr int kJoinMost = 512;  // parts of an item
 
-template <int D>
+template <int D, int kJoinThreads>
 __global__ void __launch_bounds__(kJoinThreads) kv8_join_kernel(AttnArgs a, int RT, int bf16) {
-  __shared__ float s_w[kJoinParts], s_red[kJoinThreads / 32], s_o[kJoinThreads * 4];
+  constexpr int WARPS = kJoinThreads / 32;
+  __shared__ float s_w[kJoinMost], s_red[WARPS], s_den[WARPS];
+  __shared__ __align__(16) float s_o[kJoinThreads * 4];
   pdl_wait();
   const int c = blockIdx.x, r = blockIdx.y, tid = threadIdx.x, lane = tid & 31;
   const int4 j0 = a.jobs[2 * c];
@@ -517,7 +520,7 @@ __global__ void __launch_bounds__(kJoinThreads) kv8_join_kernel(AttnArgs a, int 
   const int4 j1 = a.jobs[2 * c + 1];
   const RowOf ro = row_of(Seq{j0.x, j0.y, 0}, j0.w * RT + r, j0.z, a.group);
   if (ro.row < 0) return;
-  const int parts = min(j1.y - c + 1, kJoinParts);
+  const int parts = j1.y - c + 1;  // at most the first launch's blocks, kJoinMost
   auto slot = [&](int i) { return i == 0 ? j1.x : 2 * (c + i); };
 
   float top = -INFINITY;
@@ -531,33 +534,32 @@ __global__ void __launch_bounds__(kJoinThreads) kv8_join_kernel(AttnArgs a, int 
   if (lane == 0) s_red[tid >> 5] = top;
   __syncthreads();
 #pragma unroll
-  for (int w = 0; w < kJoinThreads / 32; ++w) top = fmaxf(top, s_red[w]);
+  for (int w = 0; w < WARPS; ++w) top = fmaxf(top, s_red[w]);
   float den = 0.f;
   for (int i = tid; i < parts; i += kJoinThreads) {
-    const float m = s_w[i], f = m == -INFINITY ? 1.f : ex2(m - top);  // sum and output 0, or NaN
+    const float f = s_w[i] == -INFINITY ? 1.f : ex2(s_w[i] - top);  // sum and output 0, or NaN
     s_w[i] = f;
     den += f * a.ml[(int64_t)slot(i) * RT + r].y;
   }
 #pragma unroll
   for (int o = 16; o; o >>= 1) den += __shfl_xor_sync(~0u, den, o);
-  __syncthreads();
-  if (lane == 0) s_red[tid >> 5] = den;
+  if (lane == 0) s_den[tid >> 5] = den;
   __syncthreads();
   den = 0.f;
 #pragma unroll
-  for (int w = 0; w < kJoinThreads / 32; ++w) den += s_red[w];
+  for (int w = 0; w < WARPS; ++w) den += s_den[w];
 
   constexpr int COLS = D / 4, GROUPS = kJoinThreads / COLS;
   const int col = tid % COLS, grp = tid / COLS;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
+#pragma unroll 8
   for (int i = grp; i < parts; i += GROUPS) {
     const float4 u = *reinterpret_cast<const float4 *>(a.part + ((int64_t)slot(i) * RT + r) * D + col * 4);
-    const float f = s_w[i];
-    acc.x = fmaf(u.x, f, acc.x);
-    acc.y = fmaf(u.y, f, acc.y);
-    acc.z = fmaf(u.z, f, acc.z);
-    acc.w = fmaf(u.w, f, acc.w);
+    const float w = s_w[i];
+    acc.x = fmaf(u.x, w, acc.x);
+    acc.y = fmaf(u.y, w, acc.y);
+    acc.z = fmaf(u.z, w, acc.z);
+    acc.w = fmaf(u.w, w, acc.w);
   }
   reinterpret_cast<float4 *>(s_o)[tid] = acc;
   __syncthreads();
@@ -569,10 +571,10 @@ __global__ void __launch_bounds__(kJoinThreads) kv8_join_kernel(AttnArgs a, int 
       acc.z += u.z;
       acc.w += u.w;
     }
-    const float f = den == 0.f ? 0.f : 1.f / (127.f * den);
+    const float g = den == 0.f ? 0.f : 1.f / (127.f * den);
     uint2 w;
-    w.x = bf16 ? Bf16::from_f32x2(acc.x * f, acc.y * f) : F16::from_f32x2(acc.x * f, acc.y * f);
-    w.y = bf16 ? Bf16::from_f32x2(acc.z * f, acc.w * f) : F16::from_f32x2(acc.z * f, acc.w * f);
+    w.x = bf16 ? Bf16::from_f32x2(acc.x * g, acc.y * g) : F16::from_f32x2(acc.x * g, acc.y * g);
+    w.y = bf16 ? Bf16::from_f32x2(acc.z * g, acc.w * g) : F16::from_f32x2(acc.z * g, acc.w * g);
     *reinterpret_cast<uint2 *>(a.out + (int64_t)ro.row * a.o_ts + (int64_t)ro.head * a.o_hs + col * 4) = w;
     if (col == 0 && a.lse)
       a.lse[(int64_t)ro.row * a.kv_heads * a.group + ro.head] =
@@ -582,7 +584,8 @@ __global__ void __launch_bounds__(kJoinThreads) kv8_join_kernel(AttnArgs a, int 
 
 // ----------------------------------------------------------------------------- launches
 struct DecodePlan {
-  int nt, grid, join;  // 8-row columns of a tile, blocks, whether an item can cross shares
+  int nt, grid, join;  // 8-row columns of a tile, blocks, threads of a join's block (0: none is needed)
+  int rows;            // of a tile that can hold something
   size_t smem, off_jobs, off_ml, off_part, total;
 };
 
@@ -598,8 +601,12 @@ static DecodePlan decode_plan(const lily_kv8_cache &C, const lily_kv8_batch &b, 
   const int64_t items = std::min<int64_t>(b.batch, T) * ((rows + RT - 1) / RT) * C.kv_heads;
   const int64_t tiles = std::max<int64_t>(1, ((int64_t)b.max_kv + 16 + tile - 1) / tile);
   if (items > INT32_MAX / tiles) return p;  // total 0: the tiles have to be countable in 31 bits
-  p.grid = (int)std::max<int64_t>(1, std::min<int64_t>(2 * sms, items * tiles));
-  p.join = tiles > 1;
+  p.grid = (int)std::max<int64_t>(1, std::min<int64_t>(std::min(2 * sms, kJoinMost), items * tiles));
+  // Few items have many parts each: a large block reads a row's parts together (262,144 tokens, 152
+  // parts: 12 us with 256 threads, 8 with 512).  Many items have two or three: small blocks start
+  // faster (64 sequences, 512 items: 6 us with 256 threads, 10 with 512).
+  p.join = tiles == 1 ? 0 : p.grid / items >= 8 ? 512 : 128;
+  p.rows = (int)std::min<int64_t>(RT, rows);
   const int ng = kTurnBytes / D / 16;
   p.smem = kDecWarps * kDecStages * 2 * kTurnBytes + RT * (D * 2 + 16) +
            4 * (kDecWarps * kDecStages * 2 * ng + RT + 2 * kDecWarps * RT + 4 + b.batch + 1);
@@ -616,11 +623,14 @@ static DecodePlan decode_plan(const lily_kv8_cache &C, const lily_kv8_batch &b, 
 template <int D, int NT>
 static cudaError_t launch_decode_shape(const AttnArgs &a, const DecodePlan &p, int bf16, cudaStream_t st) {
   auto kernel = kv8_decode_kernel<D, NT>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)p.smem);
+  static size_t allowed[64];
+  cudaError_t e = allow_smem(kernel, p.smem, allowed);
   if (e != cudaSuccess) return e;
   e = launch_pdl(kernel, dim3(p.grid), dim3(kDecThreads), p.smem, st, a, bf16);
   if (e != cudaSuccess || !p.join) return e;
-  return launch_pdl(kv8_join_kernel<D>, dim3(p.grid, 8 * NT), dim3(kJoinThreads), 0, st, a, 8 * NT, bf16);
+  const dim3 grid(p.grid, p.rows);
+  if (p.join == 512) return launch_pdl(kv8_join_kernel<D, 512>, grid, dim3(512), 0, st, a, 8 * NT, bf16);
+  return launch_pdl(kv8_join_kernel<D, 128>, grid, dim3(128), 0, st, a, 8 * NT, bf16);
 }
 
 template <int D>
@@ -638,7 +648,10 @@ static bool prompt_form(const lily_kv8_cache &C, const lily_kv8_batch &b, int q_
 }
 
 size_t kv8_attention_ws_bytes(const lily_kv8_cache &C, const lily_kv8_batch &b, int T, int q_heads) {
-  return prompt_form(C, b, q_heads) ? prompt_plan(C, b, T, q_heads).total : decode_plan(C, b, T, q_heads).total;
+  if (!prompt_form(C, b, q_heads)) return decode_plan(C, b, T, q_heads).total;
+  lily_kv8_batch fewer = b;  // the split form's largest calls, so that the space serves them too
+  fewer.max_q = std::max(1, (kPromptRows - 1) / (q_heads / C.kv_heads));
+  return std::max(decode_plan(C, fewer, T, q_heads).total, prompt_plan(C, b, T, q_heads).total);
 }
 
 int launch_kv8_attention(const lily_kv8_cache &C, const lily_kv8_batch &b, const AttnShape &s,

@@ -8,8 +8,9 @@
 // float (8 or 11 significant bits), so 127 x and q amax are exact in fp32 (at most 18 bits).  Let
 // the numerator be an integer times 2^a and amax an integer N < 2^11 times 2^b: a quotient that is
 // not an odd multiple of 1/2 differs from every such multiple by at least 2^(a-b) / (2 N), and one
-// of 1/2 or more has 2^(a-b) >= 2^-9 or so: by 4e-7 at least.  num * (1 / den) is off by 2^-22
-// relative (2e-5 at most), so it decides everything farther than 1e-3 from a tie; nearer, an IEEE
+// of 1/2 or more has 2^(a-b) >= 2^-9 or so: by 4e-7 at least.  the product with a rounded
+// 127 / amax is off by 2^-22 relative (3e-5 at most), so it decides everything farther than 1e-4 from a
+// tie; nearer, an IEEE
 // division (3e-8 off at 1/2, 2^-24 relative above) decides, and gives an exact tie exactly.
 //
 // Bound by memory: 2 bytes in and 1 byte out an element; at one token a sequence by the launch
@@ -35,11 +36,27 @@ struct CacheArgs {
 
 constexpr int kAppendThreads = 256;
 
-// rint(num / den) of exact arithmetic; num and den as described above, inv = 1 / den.
-__device__ __forceinline__ int exact_code(float num, float den, float inv) {
-  float q = num * inv;
-  if (!(fabsf(q - rintf(q)) < 0.499f)) q = __fdiv_rn(num, den);
-  return __float2int_rn(fminf(fmaxf(q, -127.f), 127.f));
+// 1.5 * 2^23: adding it rounds a number of magnitude below 2^22 to the nearest integer (ties to
+// even), which the sum then holds in its low bits, negative ones as two's complement.
+constexpr float kRound = 12582912.f;
+
+// The codes rint(x[i] up / den) of exact arithmetic, as bytes; x up and den as described above,
+// k = up / den to fp32's precision, or 0 where that is out of fp32's range.
+__device__ __forceinline__ uint32_t exact_codes4(const float (&x)[4], float up, float den, float k) {
+  float n[4], far = 0.f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float q = x[i] * k;
+    n[i] = q + kRound;
+    far = fmaxf(far, fabsf(q - (n[i] - kRound)));
+  }
+  if (far > 0.4999f || k == 0.f) {  // one of them within 1e-4 of a tie
+#pragma unroll
+    for (int i = 0; i < 4; ++i) n[i] = __fdiv_rn(x[i] * up, den) + kRound;
+  }
+  const uint32_t lo = __byte_perm(__float_as_uint(n[0]), __float_as_uint(n[1]), 0x0040);
+  const uint32_t hi = __byte_perm(__float_as_uint(n[2]), __float_as_uint(n[3]), 0x0040);
+  return __byte_perm(lo, hi, 0x5410);
 }
 
 __device__ __forceinline__ uint32_t umax16x2(uint32_t a, uint32_t b) { return __vmaxu2(a, b); }
@@ -78,10 +95,9 @@ __global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(CacheArgs a)
       t += rows;
       continue;
     }
-    const int page = check_page(B, raw_page(B, b, pos >> B.page_shift), a.hdr);
+    const int raw = raw_page(B, b, pos >> B.page_shift);  // checked below, the rows under way
     const int t_run = t;
     t += rows;
-    if (page < 0) continue;
 
     // the run's elements and their largest magnitude (as bits: NaN > infinity > finite)
     const uint16_t *x = static_cast<const uint16_t *>(a.x[kv]) + t_run * a.ts[kv] + h * a.hs[kv];
@@ -93,6 +109,8 @@ __global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(CacheArgs a)
       v[i] = make_uint4(0, 0, 0, 0);
       if (r < rows) v[i] = *reinterpret_cast<const uint4 *>(x + r * a.ts[kv] + (c - r * cpr) * 8);
     }
+    const int page = check_page(B, raw, a.hdr);
+    if (page < 0) continue;
     const int64_t ph = (int64_t)page * a.kv_heads + h;
     float *amax = a.amax[kv] + ph;
     const float was = in_page ? *amax : 0.f;
@@ -115,7 +133,7 @@ __global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(CacheArgs a)
     // a power of two that keeps 127 x, q amax and 1 / amax inside fp32's range (exact: whatever
     // underflows by it has code 0)
     const float sc = now > 0x1p60f ? 0x1p-64f : now < 0x1p-60f ? 0x1p64f : 1.f;
-    const float den = now * sc, inv = 1.f / den;
+    const float den = now * sc, inv = 1.f / den, up = 127.f * sc;
 
     int8_t *codes = a.codes[kv] + ph * B.page * a.D;
     if (in_page && __float_as_uint(now) != __float_as_uint(was)) {
@@ -125,13 +143,10 @@ __global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(CacheArgs a)
         uint32_t *u = &w.x;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          uint32_t r = 0;
+          float num[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float q = (float)(int8_t)(u[j] >> (8 * e));
-            const int n = finite ? exact_code(q * (was * sc), den, inv) : 0;
-            r |= (uint32_t)(uint8_t)n << (8 * e);
-          }
+          for (int e = 0; e < 4; ++e) num[e] = (float)(int8_t)(u[j] >> (8 * e));
+          const uint32_t r = finite ? exact_codes4(num, was * sc, den, sc == 1.f ? was * inv : 0.f) : 0;
           u[j] = r;
         }
         *reinterpret_cast<uint4 *>(codes + c * 16) = w;
@@ -144,10 +159,12 @@ __global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(CacheArgs a)
         float f[8];
         unpack8<Ty>(v[i], f);
         uint32_t r2[2] = {0, 0};
+        if (finite && !zero) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int n = finite && !zero ? exact_code(f[e] * sc * 127.f, den, inv) : 0;
-          r2[e >> 2] |= (uint32_t)(uint8_t)n << (8 * (e & 3));
+          for (int e = 0; e < 2; ++e) {
+            const float x4[4] = {f[4 * e], f[4 * e + 1], f[4 * e + 2], f[4 * e + 3]};
+            r2[e] = exact_codes4(x4, up, den, sc == 1.f ? up * inv : 0.f);
+          }
         }
         *reinterpret_cast<uint2 *>(codes + (int64_t)(in_page + r) * a.D + (c - r * cpr) * 8) =
             make_uint2(r2[0], r2[1]);
@@ -160,9 +177,10 @@ __global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(CacheArgs a)
 }
 
 // ----------------------------------------------------------------------------- read
-// A warp takes 8 tokens: lanes 0-7 find their sequences and pages together, then the warp walks
-// the tokens' 16-code chunks.  Bound by memory (1 byte in, 2 or 4 out an element).
-constexpr int kReadThreads = 256, kReadTokens = 8;
+// A warp takes 8 tokens: lanes 0-7 find their sequences and pages together, then the warp walks the
+// tokens' heads, D / 16 lanes a head and 16 codes a lane, four loads of codes in flight.  Bound by
+// memory (1 byte in, 2 or 4 out an element).
+constexpr int kReadThreads = 256, kReadTokens = 8, kReadAhead = 4;
 
 template <int DT>
 __global__ void __launch_bounds__(kReadThreads) kv8_read_kernel(CacheArgs a) {
@@ -186,44 +204,61 @@ __global__ void __launch_bounds__(kReadThreads) kv8_read_kernel(CacheArgs a) {
       }
     }
   }
-  const int per_row = a.D >> 4, per_token = per_row * a.kv_heads;
-  const int total = min(kReadTokens, B.T - t0) * per_token;
+  // heads of 8 tokens in steps of `step` = 512 / D: token i, head h of this lane's next one
+  const int step = 512 / a.D, di = step / a.kv_heads, dh = step - di * a.kv_heads;
+  const int d = (lane & (a.D / 16 - 1)) * 16;
+  int h = lane / (a.D / 16), i = h / a.kv_heads;
+  h -= i * a.kv_heads;
   const int8_t *codes = a.codes[kv];
   const float *amax = a.amax[kv];
-  for (int c0 = 0; c0 < total; c0 += 32) {
-    const int c = c0 + lane, i = min(c / per_token, kReadTokens - 1);
-    const int p = __shfl_sync(~0u, page, i), r = __shfl_sync(~0u, in_page, i);
-    if (c >= total || p == -2) continue;
-    const int j = c - i * per_token, h = j / per_row, d = (j - h * per_row) * 16;
-    float f[16];
-    if (p < 0) {
+  const int rounds = (kReadTokens * a.kv_heads + step - 1) / step;
+  for (int r0 = 0; r0 < rounds; r0 += kReadAhead) {
+    uint4 w[kReadAhead];
+    float s[kReadAhead];
+    int64_t at[kReadAhead];  // where the values go, or -1
 #pragma unroll
-      for (int e = 0; e < 16; ++e) f[e] = 0.f;
-    } else {
-      const int64_t ph = (int64_t)p * a.kv_heads + h;
-      const uint4 w = *reinterpret_cast<const uint4 *>(codes + (ph * B.page + r) * a.D + d);
-      const float s = __ldg(amax + ph);
-      const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-      for (int e = 0; e < 16; ++e) f[e] = __fdiv_rn((float)(int8_t)(u[e >> 2] >> (8 * (e & 3))) * s, 127.f);
-    }
-    const int64_t off = (int64_t)(t0 + i) * a.ts[kv] + (int64_t)h * a.hs[kv] + d;
-    if (DT == LILY_F32) {
-      float *o = static_cast<float *>(a.y[kv]) + off;
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        *reinterpret_cast<float4 *>(o + 4 * e) = make_float4(f[4 * e], f[4 * e + 1], f[4 * e + 2], f[4 * e + 3]);
-    } else {
-      uint16_t *o = static_cast<uint16_t *>(a.y[kv]) + off;
-      float lo[8], hi[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        lo[e] = f[e];
-        hi[e] = f[8 + e];
+    for (int r = 0; r < kReadAhead; ++r) {
+      const int src = min(i, kReadTokens - 1);
+      const int p = __shfl_sync(~0u, page, src), row = __shfl_sync(~0u, in_page, src);
+      at[r] = i < kReadTokens && p != -2 ? (int64_t)(t0 + i) * a.ts[kv] + (int64_t)h * a.hs[kv] + d : -1;
+      const int64_t ph = (int64_t)max(p, 0) * a.kv_heads + h;
+      w[r] = make_uint4(0, 0, 0, 0);
+      s[r] = 0.f;
+      if (at[r] >= 0 && p >= 0) {
+        w[r] = __ldg(reinterpret_cast<const uint4 *>(codes + (ph * B.page + row) * a.D + d));
+        s[r] = __ldg(amax + ph);
       }
-      using Ty = typename std::conditional<DT == LILY_BF16, Bf16, F16>::type;
-      *reinterpret_cast<uint4 *>(o) = pack8<Ty>(lo);
-      *reinterpret_cast<uint4 *>(o + 8) = pack8<Ty>(hi);
+      i += di;
+      h += dh;
+      if (h >= a.kv_heads) {
+        h -= a.kv_heads;
+        ++i;
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < kReadAhead; ++r) {
+      if (at[r] < 0) continue;
+      float f[16];
+      const uint32_t u[4] = {w[r].x, w[r].y, w[r].z, w[r].w};
+#pragma unroll
+      for (int e = 0; e < 16; ++e) f[e] = (float)(int8_t)(u[e >> 2] >> (8 * (e & 3))) * s[r] * (1.f / 127.f);
+      if (DT == LILY_F32) {
+        float *o = static_cast<float *>(a.y[kv]) + at[r];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          *reinterpret_cast<float4 *>(o + 4 * e) = make_float4(f[4 * e], f[4 * e + 1], f[4 * e + 2], f[4 * e + 3]);
+      } else {
+        uint16_t *o = static_cast<uint16_t *>(a.y[kv]) + at[r];
+        float lo[8], hi[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          lo[e] = f[e];
+          hi[e] = f[8 + e];
+        }
+        using Ty = typename std::conditional<DT == LILY_BF16, Bf16, F16>::type;
+        *reinterpret_cast<uint4 *>(o) = pack8<Ty>(lo);
+        *reinterpret_cast<uint4 *>(o + 8) = pack8<Ty>(hi);
+      }
     }
   }
 }

@@ -748,23 +748,23 @@ PromptPlan prompt_plan(const lily_kv8_cache &C, const lily_kv8_batch &b, int T, 
   // share costs its block's start and a write and read of its output).
   p.items = (int)items;
   p.splits = (int)std::max<int64_t>(1, std::min<int64_t>(sms / items, tiles / 4));
-  p.total = kAlign;
-  if (p.splits > 1) {
-    size_t off = kAlign;
-    p.off_jobs = off;
-    off = align_up(off + items * sizeof(int4));
-    p.off_ml = off;
-    off = align_up(off + items * p.splits * R * sizeof(float2));
-    p.off_part = off;
-    p.total = align_up(off + (size_t)items * p.splits * R * D * sizeof(float));
-  }
+  // The space is that of sms parts, which any number of row tiles keeps to, so that a workspace
+  // serves smaller calls too.
+  size_t off = kAlign;
+  p.off_jobs = off;
+  off = align_up(off + sms * sizeof(int4));
+  p.off_ml = off;
+  off = align_up(off + sms * R * sizeof(float2));
+  p.off_part = off;
+  p.total = tiles >= 8 ? align_up(off + (size_t)sms * R * D * sizeof(float)) : kAlign;
   return p;
 }
 
 template <int D>
 static cudaError_t launch_prompt_dim(const AttnArgs &a, const PromptPlan &p, int bf16, cudaStream_t st) {
   using P = PromptShape<D>;
-  cudaError_t e = cudaFuncSetAttribute(kv8_prompt_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, P::SMEM);
+  static size_t allowed[64];
+  cudaError_t e = allow_smem(kv8_prompt_kernel<D>, P::SMEM, allowed);
   if (e != cudaSuccess) return e;
   e = launch_pdl(kv8_prompt_kernel<D>, dim3(p.items, p.splits), dim3(P::THREADS), P::SMEM, st, a, bf16, p.splits);
   if (e != cudaSuccess || p.splits == 1) return e;

@@ -387,8 +387,8 @@ LILY_Q4_API int lily_kv8_append(const lily_kv8_cache *cache, const lily_kv8_batc
                                 size_t ws_bytes, lily_q4_stream_t stream);
 
 /*
- * lily_kv8_read -- the values of the batch's tokens, q * amax / 127 rounded once to dtype
- * (LILY_BF16, LILY_F16 or LILY_F32): the inverse of lily_kv8_append, for moving a prefix to
+ * lily_kv8_read -- the values of the batch's tokens, q * amax / 127 (in fp32: q amax is exact,
+ * times 1/127, 2^-23 relative) rounded to dtype (LILY_BF16, LILY_F16 or LILY_F32): the inverse of lily_kv8_append, for moving a prefix to
  * another cache or checking one.
  */
 LILY_Q4_API int lily_kv8_read(const lily_kv8_cache *cache, const lily_kv8_batch *batch, int32_t T,

@@ -159,7 +159,7 @@ def test_attention_workspace(lib):
     size = lambda c, b, T, h: lib.lily_kv8_attention_workspace_bytes(C.byref(c), C.byref(b), T, h)
     assert size(_cache(), _batch(), 6, 7) == 0
     assert size(_cache(page=8), _batch(), 6, 8) == 0
-    assert size(_cache(), _batch(max_q=1 << 30, max_kv=1 << 30, batch=4096), 1 << 30, 256) == 0  # uncountable
+    assert size(_cache(), _batch(max_q=1, max_kv=1 << 30, batch=4096), 4096, 8) == 0  # uncountable
     last = 0
     for max_q, T in ((1, 3), (4, 12), (200, 600), (4096, 9000)):
         n = size(_cache(), _batch(max_q=max_q, max_kv=5000), T, 16)
