@@ -503,18 +503,34 @@ __global__ void __launch_bounds__(kDecThreads, 2) kv8_decode_kernel(AttnArgs a, 
 }
 
 // ----------------------------------------------------------------------------- join
-// Block (c, r): row r of the item that block c of the first launch began and did not finish.  The
-// parts' maxima and sums first (a thread each), then the outputs: a quarter of a head's four-element
+// Block (c, r): row r of the item that block c of the first launch began and did not finish (blocks of
+// kJoinMost threads: of the c-th of these, so that few blocks are launched).  The parts' maxima and sums first (a thread each), then the outputs: a quarter of a head's four-element
 // columns take the parts in turns, eight loads in flight a thread.
 constexpr int kJoinMost = 512;  // parts of an item
 
 template <int D, int kJoinThreads>
-__global__ void __launch_bounds__(kJoinThreads) kv8_join_kernel(AttnArgs a, int RT, int bf16) {
+__global__ void __launch_bounds__(kJoinThreads) kv8_join_kernel(AttnArgs a, int RT, int bf16, int blocks) {
   constexpr int WARPS = kJoinThreads / 32;
   __shared__ float s_w[kJoinMost], s_red[WARPS], s_den[WARPS];
+  __shared__ int s_count[WARPS], s_job;
   __shared__ __align__(16) float s_o[kJoinThreads * 4];
   pdl_wait();
-  const int c = blockIdx.x, r = blockIdx.y, tid = threadIdx.x, lane = tid & 31;
+  const int r = blockIdx.y, tid = threadIdx.x, lane = tid & 31;
+  int c = blockIdx.x;
+  if (kJoinThreads == kJoinMost) {
+    // block i takes the i-th of the jobs that there are
+    const bool job = tid < blocks && a.jobs[2 * tid].x >= 0;
+    const uint32_t some = __ballot_sync(~0u, job);
+    if (tid == 0) s_job = -1;
+    if (lane == 0) s_count[tid >> 5] = __popc(some);
+    __syncthreads();
+    int before = __popc(some & ((1u << lane) - 1));
+    for (int w = 0; w < tid >> 5; ++w) before += s_count[w];
+    if (job && before == (int)blockIdx.x) s_job = tid;
+    __syncthreads();
+    c = s_job;
+    if (c < 0) return;
+  }
   const int4 j0 = a.jobs[2 * c];
   if (j0.x < 0) return;
   const int4 j1 = a.jobs[2 * c + 1];
@@ -585,7 +601,7 @@ __global__ void __launch_bounds__(kJoinThreads) kv8_join_kernel(AttnArgs a, int 
 // ----------------------------------------------------------------------------- launches
 struct DecodePlan {
   int nt, grid, join;  // 8-row columns of a tile, blocks, threads of a join's block (0: none is needed)
-  int rows;            // of a tile that can hold something
+  int rows, items;     // of a tile that can hold something; items, at most the blocks
   size_t smem, off_jobs, off_ml, off_part, total;
 };
 
@@ -605,7 +621,8 @@ static DecodePlan decode_plan(const lily_kv8_cache &C, const lily_kv8_batch &b, 
   // Few items have many parts each: a large block reads a row's parts together (262,144 tokens, 152
   // parts: 12 us with 256 threads, 8 with 512).  Many items have two or three: small blocks start
   // faster (64 sequences, 512 items: 6 us with 256 threads, 10 with 512).
-  p.join = tiles == 1 ? 0 : p.grid / items >= 8 ? 512 : 128;
+  p.join = tiles == 1 ? 0 : p.grid / items >= 8 ? kJoinMost : 128;
+  p.items = (int)std::min<int64_t>(items, p.grid);
   p.rows = (int)std::min<int64_t>(RT, rows);
   const int ng = kTurnBytes / D / 16;
   p.smem = kDecWarps * kDecStages * 2 * kTurnBytes + RT * (D * 2 + 16) +
@@ -628,9 +645,9 @@ static cudaError_t launch_decode_shape(const AttnArgs &a, const DecodePlan &p, i
   if (e != cudaSuccess) return e;
   e = launch_pdl(kernel, dim3(p.grid), dim3(kDecThreads), p.smem, st, a, bf16);
   if (e != cudaSuccess || !p.join) return e;
-  const dim3 grid(p.grid, p.rows);
-  if (p.join == 512) return launch_pdl(kv8_join_kernel<D, 512>, grid, dim3(512), 0, st, a, 8 * NT, bf16);
-  return launch_pdl(kv8_join_kernel<D, 128>, grid, dim3(128), 0, st, a, 8 * NT, bf16);
+  if (p.join == kJoinMost)
+    return launch_pdl(kv8_join_kernel<D, kJoinMost>, dim3(p.items, p.rows), dim3(kJoinMost), 0, st, a, 8 * NT, bf16, p.grid);
+  return launch_pdl(kv8_join_kernel<D, 128>, dim3(p.grid, p.rows), dim3(128), 0, st, a, 8 * NT, bf16, p.grid);
 }
 
 template <int D>

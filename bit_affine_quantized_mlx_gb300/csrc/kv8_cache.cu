@@ -34,8 +34,6 @@ struct CacheArgs {
   int kv_heads, D, chunk;
 };
 
-constexpr int kAppendThreads = 256;
-
 // 1.5 * 2^23: adding it rounds a number of magnitude below 2^22 to the nearest integer (ties to
 // even), which the sum then holds in its low bits, negative ones as two's complement.
 constexpr float kRound = 12582912.f;
@@ -62,15 +60,15 @@ __device__ __forceinline__ uint32_t exact_codes4(const float (&x)[4], float up, 
 __device__ __forceinline__ uint32_t umax16x2(uint32_t a, uint32_t b) { return __vmaxu2(a, b); }
 
 // TEAM threads handle a run; NV chunks of 8 elements a thread hold it (TEAM * NV * 8 >= its size).
-// TEAM = 32 (short runs: decode): a block has 8 teams, one token each.  TEAM = 256: the block
-// walks the runs that start among its `chunk` tokens.
-template <typename Ty, int TEAM, int NV>
-__global__ void __launch_bounds__(kAppendThreads) kv8_append_kernel(CacheArgs a) {
-  __shared__ uint32_t s_max[kAppendThreads / 32];
+// A team walks the runs that start among its `chunk` tokens.  Teams of one warp need no barrier and
+// share a block.
+template <typename Ty, int TEAM, int TEAMS, int NV>
+__global__ void __launch_bounds__(TEAM *TEAMS) kv8_append_kernel(CacheArgs a) {
+  static_assert(TEAM == 32 || TEAMS == 1, "a block barrier joins a team");
+  __shared__ uint32_t s_max[TEAM / 32];
   pdl_wait();
   const Batch &B = a.B;
   const int tid = threadIdx.x & (TEAM - 1), team = threadIdx.x / TEAM;
-  constexpr int TEAMS = kAppendThreads / TEAM;
   const int h = blockIdx.y, kv = blockIdx.z;
   const int cpr = a.D >> 3;  // chunks of 8 a row
   const int t_first = (blockIdx.x * TEAMS + team) * a.chunk;
@@ -296,26 +294,21 @@ static CacheArgs cache_args(const lily_kv8_cache &C, const lily_kv8_batch &b, in
 template <typename Ty>
 static cudaError_t launch_append(CacheArgs &a, cudaStream_t st) {
   const int D = a.D, T = a.B.T;
-  const dim3 block(kAppendThreads);
-  // Runs of at most 4 * 32 chunks (one token of 256, four of 64 ...) are held by one warp, eight
-  // runs a block; with a block a run, its other seven warps would idle.
   const int most = std::min(a.B.max_q, a.B.page);  // rows of the longest run
-  if (most * (D / 8) <= 128) {
-    a.chunk = 1;
-    const dim3 grid((T + 7) / 8, a.kv_heads, 2);
-    return launch_pdl(kv8_append_kernel<Ty, 32, 4>, grid, block, 0, st, a);
-  }
-  // Tokens of a block: about one sequence's or one page's worth, so that it walks one or two runs.
-  int chunk = 1;
-  while (chunk * 2 <= std::min(a.B.page, T / a.B.batch)) chunk *= 2;
-  a.chunk = chunk;
-  const dim3 grid((T + chunk - 1) / chunk, a.kv_heads, 2);
   const int nv = most * (D / 8);
-  if (nv <= 256) return launch_pdl(kv8_append_kernel<Ty, 256, 1>, grid, block, 0, st, a);
-  if (nv <= 512) return launch_pdl(kv8_append_kernel<Ty, 256, 2>, grid, block, 0, st, a);
-  if (nv <= 1024) return launch_pdl(kv8_append_kernel<Ty, 256, 4>, grid, block, 0, st, a);
-  if (nv <= 2048) return launch_pdl(kv8_append_kernel<Ty, 256, 8>, grid, block, 0, st, a);
-  return launch_pdl(kv8_append_kernel<Ty, 256, 16>, grid, block, 0, st, a);
+  // Tokens of a team: about one sequence's or one page's worth, so that it walks one or two runs.
+  int chunk = 1;
+  while (chunk * 2 <= std::min(most, T / a.B.batch)) chunk *= 2;
+  a.chunk = chunk;
+  const int walks = (T + chunk - 1) / chunk;
+  // The threads that hold a run in 32 registers each.
+  if (nv <= 128) return launch_pdl(kv8_append_kernel<Ty, 32, 8, 4>, dim3((walks + 7) / 8, a.kv_heads, 2), dim3(256), 0, st, a);
+  if (nv <= 256) return launch_pdl(kv8_append_kernel<Ty, 32, 4, 8>, dim3((walks + 3) / 4, a.kv_heads, 2), dim3(128), 0, st, a);
+  const dim3 grid(walks, a.kv_heads, 2);
+  if (nv <= 512) return launch_pdl(kv8_append_kernel<Ty, 64, 1, 8>, grid, dim3(64), 0, st, a);
+  if (nv <= 1024) return launch_pdl(kv8_append_kernel<Ty, 128, 1, 8>, grid, dim3(128), 0, st, a);
+  if (nv <= 2048) return launch_pdl(kv8_append_kernel<Ty, 256, 1, 8>, grid, dim3(256), 0, st, a);
+  return launch_pdl(kv8_append_kernel<Ty, 512, 1, 8>, grid, dim3(512), 0, st, a);
 }
 
 static int status_of(cudaError_t e) {

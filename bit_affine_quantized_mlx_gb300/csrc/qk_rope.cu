@@ -3,10 +3,11 @@
 //   y = x * rsqrt(mean(x^2) + eps) * (w + offset);   (y_a, y_b) rotated by pos * f
 //
 // Bound by memory: each head is read and written once (4 bytes an element); at small T by the
-// launch.  A block takes tokens and all their heads (or a share of them when there are few
-// tokens), because the angles are the token's: their sines are computed once a token into shared
-// memory, not once a head, and a lane keeps its own for all its heads.  A head is held by a power of
-// two of lanes, 8 elements in each: 8 neighbours, or, where the first R elements turn in half pairs,
+// launch.  A warp takes a token and all its heads (a share of them when there are few tokens),
+// because the angles are the token's: their sines are computed once, and
+// passed through shared memory of the warp's own to the lanes that keep them for all their heads; no
+// barrier of the block is needed.  A head is held by 8, 16
+// or 32 lanes, 8 elements in each: 8 neighbours, or, where the first R elements turn in half pairs,
 // 4 of the lower half and their 4 partners of the upper.  So both elements of a pair are always in
 // one lane and only the sum of squares is exchanged.  R / 2 that is not a multiple of 4 breaks the
 // half pairs' runs of four: those heads go through shared memory.
@@ -15,121 +16,119 @@
 // 64-bit integers is the angle of any 32-bit position without loss; its top 32 bits, taken as
 // signed, are the angle in [-1/2, 1/2) turns, which sincospif takes after a rounding of
 // 2^-24 relative.  A 32-bit float product would be off by 0.06 rad at position 10^6.
+#include <algorithm>
 #include <cmath>
 
 #include "kv8_device.cuh"
 
 namespace lq4 {
 
+struct RopeRows {  // q or k
+  const uint16_t *in, *weight;
+  uint16_t *out;
+  int64_t in_ts, in_hs, out_ts, out_hs;
+  int heads;
+};
 struct RopeArgs {
+  RopeRows part[2];
   const int32_t *pos;
-  const void *in[2];
-  void *out[2];
-  const void *weight[2];
-  int64_t in_ts[2], in_hs[2], out_ts[2], out_hs[2];
   const uint64_t *turns;
   float eps, offset, rope_scale;
-  int T, q_heads, heads, D, R, lanes_shift, normalize;
+  int T, D, R, normalize;
 };
 
-constexpr int kRopeThreads = 256;
+constexpr int kRopeWarps = 4, kRopeAhead = 4;
 enum RopePairs { kPairsNear, kPairsHalf, kPairsHalfOdd };
 
-// PASSES: heads a lane group takes in one go.  A block walks tokens gridDim.x apart; the next
-// token's first heads are loaded before the current one's are computed.
-template <typename Ty, int PAIRS, int PASSES>
-__global__ void __launch_bounds__(kRopeThreads, PAIRS == kPairsHalfOdd ? 3 : 5)
-    qk_norm_rope_kernel(RopeArgs a) {
-  __shared__ __align__(16) float2 s_cs[2][128];
-  __shared__ float s_row[PAIRS == kPairsHalfOdd ? (kRopeThreads / 32) * 256 : 1];
+// LANES a head; kRopeAhead passes (32 / LANES heads each) are loaded together.
+template <typename Ty, int PAIRS, int LANES>
+__global__ void __launch_bounds__(32 * kRopeWarps, PAIRS == kPairsHalfOdd ? 6 : 9)
+    qk_norm_rope_kernel(RopeArgs a, int shares) {
+  constexpr int GROUPS = 32 / LANES;
+  __shared__ __align__(16) float2 s_cs[kRopeWarps][128];
+  __shared__ float s_row[PAIRS == kPairsHalfOdd ? kRopeWarps * 256 : 1];
   pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int lanes = 1 << a.lanes_shift, c = lane & (lanes - 1);
-  const int groups = kRopeThreads >> a.lanes_shift;
-  const int g = threadIdx.x >> a.lanes_shift;
+  const int64_t task = (int64_t)blockIdx.x * kRopeWarps + warp;
+  const int t = (int)(task / shares), share = (int)(task - (int64_t)t * shares);
+  if (t >= a.T) return;
+  const int c = lane & (LANES - 1), g = lane / LANES;
   const bool live = c * 8 < a.D;
   const int half = a.R >> 1;
   // this lane's elements: e0 .. e0 + 3 and e1 .. e1 + 3
-  const bool split = PAIRS == kPairsHalf && c * 8 < a.R;
-  const int e0 = live ? (split ? 4 * c : 8 * c) : 0, e1 = live ? (split ? half + 4 * c : 8 * c + 4) : 0;
-  const bool turns = PAIRS != kPairsHalfOdd && live && 4 * c < half;
-  // this block's heads
-  const int per = (a.heads + gridDim.y - 1) / gridDim.y;
-  const int h_begin = blockIdx.y * per, h_end = min(a.heads, h_begin + per);
-
-  uint2 raw[PASSES][2];
-  auto load = [&](int t, int base) {
-#pragma unroll
-    for (int i = 0; i < PASSES; ++i) {
-      const int h = base + i * groups + g;
-      raw[i][0] = raw[i][1] = make_uint2(0, 0);
-      if (t < a.T && h < h_end && live) {
-        const int w = h >= a.q_heads;
-        const uint16_t *src = static_cast<const uint16_t *>(a.in[w]) + t * a.in_ts[w] +
-                              (int64_t)(w ? h - a.q_heads : h) * a.in_hs[w];
-        raw[i][0] = *reinterpret_cast<const uint2 *>(src + e0);
-        raw[i][1] = *reinterpret_cast<const uint2 *>(src + e1);
-      }
-    }
-  };
-  load(blockIdx.x, h_begin);
-  auto angles = [&](int t, int buf) {
-    if (t < a.T && (int)threadIdx.x < half) {
-      const uint64_t turn = (uint64_t)(int64_t)a.pos[t] * a.turns[threadIdx.x];
-      float sn, cs;
-      sincospif((float)(int32_t)(turn >> 32) * 0x1p-31f, &sn, &cs);
-      s_cs[buf][threadIdx.x] = make_float2(cs * a.rope_scale, sn * a.rope_scale);
-    }
-  };
-  angles(blockIdx.x, 0);
-  uint2 wraw[2][2] = {};
-  if (a.normalize && live) {
-#pragma unroll
-    for (int w = 0; w < 2; ++w) {
-      if (!a.weight[w]) continue;
-      const uint16_t *src = static_cast<const uint16_t *>(a.weight[w]);
-      wraw[w][0] = *reinterpret_cast<const uint2 *>(src + e0);
-      wraw[w][1] = *reinterpret_cast<const uint2 *>(src + e1);
-    }
-  }
+  const bool apart = PAIRS == kPairsHalf && c * 8 < a.R;
+  const int e0 = live ? (apart ? 4 * c : 8 * c) : 0, e1 = live ? (apart ? half + 4 * c : 8 * c + 4) : 0;
+  // this warp's heads, queries' first
+  const int heads = a.part[0].heads + a.part[1].heads, per = (heads + shares - 1) / shares;
+  const int from = share * per, to = min(heads, from + per);
+  float2 *cs_of = s_cs[warp];
+  float2 cs[4];
+  bool angles = false;
   const float inv_d = 1.f / (float)a.D;
-  int buf = 0;
-  for (int t = blockIdx.x; t < a.T; t += gridDim.x, buf ^= 1) {
-    __syncthreads();  // this token's sines are there, the last one's have been read
-    const float2 *cs_of = s_cs[buf];
-    float2 cs[4];
+
 #pragma unroll
-    for (int j = 0; j < 4; ++j) cs[j] = turns && 4 * c + j < half ? cs_of[4 * c + j] : make_float2(1.f, 0.f);
-    for (int base = h_begin; base < h_end; base += PASSES * groups) {
-      uint2 cur[PASSES][2];
+  for (int w = 0; w < 2; ++w) {
+    const RopeRows &p = a.part[w];
+    const int skip = w ? a.part[0].heads : 0;
+    const int h_begin = max(from - skip, 0), h_end = min(to - skip, p.heads);
+    if (h_begin >= h_end) continue;
+    const uint16_t *src = p.in + t * p.in_ts + (int64_t)(h_begin + g) * p.in_hs;
+    uint16_t *dst = p.out + t * p.out_ts + (int64_t)(h_begin + g) * p.out_hs;
+    const int64_t in_step = GROUPS * p.in_hs, out_step = GROUPS * p.out_hs;
+    int left = live ? h_end - h_begin - g : 0;  // heads of this lane's group still to do, times GROUPS
+    uint2 raw[kRopeAhead][2];
+    auto load = [&]() {
 #pragma unroll
-      for (int i = 0; i < PASSES; ++i) cur[i][0] = raw[i][0], cur[i][1] = raw[i][1];
-      const bool last = base + PASSES * groups >= h_end;
-      load(last ? t + gridDim.x : t, last ? h_begin : base + PASSES * groups);
-      if (last) angles(t + gridDim.x, buf ^ 1);
+      for (int i = 0; i < kRopeAhead; ++i) {
+        raw[i][0] = raw[i][1] = make_uint2(0, 0);
+        if (left > i * GROUPS) {
+          raw[i][0] = *reinterpret_cast<const uint2 *>(src + i * in_step + e0);
+          raw[i][1] = *reinterpret_cast<const uint2 *>(src + i * in_step + e1);
+        }
+      }
+    };
+    load();
+    float wt[8];
 #pragma unroll
-      for (int i = 0; i < PASSES; ++i) {
-        const int h = base + i * groups + g;
-        if (base + i * groups >= h_end) break;  // the same for every thread of the block
-        const int w = h >= a.q_heads;
+    for (int j = 0; j < 8; ++j) wt[j] = 1.f;
+    if (a.normalize && p.weight) {
+      const uint2 lo = *reinterpret_cast<const uint2 *>(p.weight + e0), hi = *reinterpret_cast<const uint2 *>(p.weight + e1);
+      unpack8<Ty>(make_uint4(lo.x, lo.y, hi.x, hi.y), wt);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) wt[j] += a.offset;
+    }
+    if (!angles) {  // the loads are under way
+      angles = true;
+      if (half > 0) {
+        const uint64_t pos = (uint64_t)(int64_t)a.pos[t];
+        for (int i = lane; i < half; i += 32) {
+          float sn, co;
+          sincospif((float)(int32_t)((pos * a.turns[i]) >> 32) * 0x1p-31f, &sn, &co);
+          cs_of[i] = make_float2(co * a.rope_scale, sn * a.rope_scale);
+        }
+        __syncwarp();
+      }
+      // pairs beyond R turn by nothing
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        cs[j] = PAIRS != kPairsHalfOdd && live && 4 * c + j < half ? cs_of[4 * c + j] : make_float2(1.f, 0.f);
+    }
+    for (int base = h_begin; base < h_end; base += kRopeAhead * GROUPS) {
+      if (base > h_begin) load();
+#pragma unroll
+      for (int i = 0; i < kRopeAhead; ++i) {
+        if (base + i * GROUPS >= h_end) break;  // the same for every lane
         float y[8];
-        unpack8<Ty>(make_uint4(cur[i][0].x, cur[i][0].y, cur[i][1].x, cur[i][1].y), y);
+        unpack8<Ty>(make_uint4(raw[i][0].x, raw[i][0].y, raw[i][1].x, raw[i][1].y), y);
         if (a.normalize) {
           float ss = 0.f;
 #pragma unroll
           for (int j = 0; j < 8; ++j) ss = fmaf(y[j], y[j], ss);
-          for (int o = lanes >> 1; o; o >>= 1) ss += __shfl_xor_sync(~0u, ss, o);
+#pragma unroll
+          for (int o = LANES / 2; o; o >>= 1) ss += __shfl_xor_sync(~0u, ss, o);
           const float rs = rsqrtf(fmaf(ss, inv_d, a.eps));
-          if (w ? a.weight[1] != nullptr : a.weight[0] != nullptr) {
-            float wt[8];
-            unpack8<Ty>(w ? make_uint4(wraw[1][0].x, wraw[1][0].y, wraw[1][1].x, wraw[1][1].y)
-                          : make_uint4(wraw[0][0].x, wraw[0][0].y, wraw[0][1].x, wraw[0][1].y), wt);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) y[j] *= rs * (wt[j] + a.offset);
-          } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) y[j] *= rs;
-          }
+          for (int j = 0; j < 8; ++j) y[j] *= rs * wt[j];
         }
         if (PAIRS == kPairsHalfOdd) {
           float *row = s_row + warp * 256 + (lane - c) * 8;
@@ -147,10 +146,9 @@ __global__ void __launch_bounds__(kRopeThreads, PAIRS == kPairsHalfOdd ? 3 : 5)
               y[j] = low ? y[j] * k.x - other * k.y : other * k.y + y[j] * k.x;
             }
           }
-        } else if (turns) {
+        } else {
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            if (PAIRS == kPairsNear && 4 * c + j >= half) break;
             float &u = PAIRS == kPairsNear ? y[2 * j] : y[j];
             float &v = PAIRS == kPairsNear ? y[2 * j + 1] : y[4 + j];
             const float x = u * cs[j].x - v * cs[j].y;
@@ -158,31 +156,36 @@ __global__ void __launch_bounds__(kRopeThreads, PAIRS == kPairsHalfOdd ? 3 : 5)
             u = x;
           }
         }
-        if (h < h_end && live) {
-          uint16_t *dst = static_cast<uint16_t *>(a.out[w]) + t * a.out_ts[w] +
-                          (int64_t)(w ? h - a.q_heads : h) * a.out_hs[w];
+        if (left > i * GROUPS) {
           const uint4 o = pack8<Ty>(y);
-          *reinterpret_cast<uint2 *>(dst + e0) = make_uint2(o.x, o.y);
-          *reinterpret_cast<uint2 *>(dst + e1) = make_uint2(o.z, o.w);
+          *reinterpret_cast<uint2 *>(dst + i * out_step + e0) = make_uint2(o.x, o.y);
+          *reinterpret_cast<uint2 *>(dst + i * out_step + e1) = make_uint2(o.z, o.w);
         }
       }
+      src += kRopeAhead * in_step;
+      dst += kRopeAhead * out_step;
+      left -= kRopeAhead * GROUPS;
     }
   }
 }
 
+template <typename Ty, int PAIRS, int LANES>
+static cudaError_t launch_lanes(const RopeArgs &a, cudaStream_t st) {
+  // A token's heads are shared out until there are about three warps for each that fits on the GPU,
+  // down to one pass a warp, at the price of computing the token's sines in each.
+  const int passes = (a.part[0].heads + a.part[1].heads + 32 / LANES - 1) / (32 / LANES);
+  const int sms = sm_count() > 0 ? sm_count() : 1;
+  const int shares = std::max(1, std::min(passes, 3 * 36 * sms / a.T));
+  const int64_t tasks = (int64_t)a.T * shares;
+  return launch_pdl(qk_norm_rope_kernel<Ty, PAIRS, LANES>, dim3((unsigned)((tasks + kRopeWarps - 1) / kRopeWarps)),
+                    dim3(32 * kRopeWarps), 0, st, a, shares);
+}
+
 template <typename Ty, int PAIRS>
 static cudaError_t launch_pairs(const RopeArgs &a, cudaStream_t st) {
-  const int groups = kRopeThreads >> a.lanes_shift;
-  // Enough blocks for every SM: with fewer tokens than that a token's heads are shared out, down
-  // to one pass a block, at the price of computing its sines in each.
-  const int passes = (a.heads + groups - 1) / groups;
-  const int sms = sm_count() > 0 ? sm_count() : 1;
-  const int split = max(1, min(passes, 2 * sms / a.T));
-  // more tokens than resident blocks: the blocks walk them
-  const dim3 grid(min(a.T, 6 * sms), split);
-  if ((passes + split - 1) / split <= 1)
-    return launch_pdl(qk_norm_rope_kernel<Ty, PAIRS, 1>, grid, dim3(kRopeThreads), 0, st, a);
-  return launch_pdl(qk_norm_rope_kernel<Ty, PAIRS, 3>, grid, dim3(kRopeThreads), 0, st, a);
+  if (a.D <= 64) return launch_lanes<Ty, PAIRS, 8>(a, st);
+  if (a.D <= 128) return launch_lanes<Ty, PAIRS, 16>(a, st);
+  return launch_lanes<Ty, PAIRS, 32>(a, st);
 }
 
 template <typename Ty>
@@ -196,29 +199,21 @@ int launch_qk_norm_rope(const lily_qk_rope &op, int T, int q_heads, int k_heads,
                         const Rows &q, const Rows &q_out, const Rows &k, const Rows &k_out,
                         cudaStream_t st) {
   RopeArgs a = {};
-  a.pos = pos;
   const Rows *in[2] = {&q, &k}, *out[2] = {&q_out, &k_out};
-  for (int w = 0; w < 2; ++w) {
-    a.in[w] = in[w]->p;
-    a.in_ts[w] = in[w]->ts;
-    a.in_hs[w] = in[w]->hs;
-    a.out[w] = out[w]->p;
-    a.out_ts[w] = out[w]->ts;
-    a.out_hs[w] = out[w]->hs;
-  }
-  a.weight[0] = op.q_weight;
-  a.weight[1] = op.k_weight;
+  const void *weight[2] = {op.q_weight, op.k_weight};
+  for (int w = 0; w < 2; ++w)
+    a.part[w] = RopeRows{static_cast<const uint16_t *>(in[w]->p), static_cast<const uint16_t *>(weight[w]),
+                         static_cast<uint16_t *>(out[w]->p), in[w]->ts, in[w]->hs, out[w]->ts, out[w]->hs,
+                         w ? k_heads : q_heads};
+  a.pos = pos;
   a.turns = op.turns;
   a.eps = op.eps;
   a.offset = op.weight_offset;
   a.rope_scale = op.rope_scale;
   a.T = T;
-  a.q_heads = q_heads;
-  a.heads = q_heads + k_heads;
   a.D = op.head_dim;
   a.R = op.rotary_dim;
   a.normalize = op.normalize;
-  while ((8 << a.lanes_shift) < a.D) ++a.lanes_shift;
   const cudaError_t e = op.dtype == LILY_BF16 ? launch_type<Bf16>(a, op.interleaved, st)
                                               : launch_type<F16>(a, op.interleaved, st);
   return e == cudaSuccess ? LILY_Q4_OK : (cudaGetLastError(), LILY_Q4_ERR_CUDA);
