@@ -39,6 +39,7 @@ struct PromptShape {
   static constexpr int ROWS = kRows * NQ;
   static constexpr int TILE = kKeys * D * 2;    // bytes of a K or V tile (and of 128 rows of Q)
   static constexpr int VW = D == 64 ? 2 : 4;    // words of a token a lane holds of V
+  static constexpr int COLS = D == 256 ? 16 : 32;  // score columns a thread holds, twice
   static constexpr int SMEM = (NQ + 2 * KB) * TILE + 1024;
 };
 
@@ -67,7 +68,7 @@ __device__ __forceinline__ void tm_ld32(uint32_t addr, float (&v)[32]) {
 }
 
 // 16 columns in two steps, for work between them; the wait passes the registers through.
-__device__ __forceinline__ void tm_ld16_start(uint32_t addr, uint32_t (&r)[16]) {
+__device__ __forceinline__ void tm_ld16_start(uint32_t addr, uint32_t *r) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
       "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
@@ -77,7 +78,7 @@ __device__ __forceinline__ void tm_ld16_start(uint32_t addr, uint32_t (&r)[16]) 
       : "r"(addr)
       : "memory");
 }
-__device__ __forceinline__ void tm_ld16_wait(uint32_t (&r)[16]) {
+__device__ __forceinline__ void tm_ld16_wait(uint32_t *r) {
   asm volatile("tcgen05.wait::ld.sync.aligned;"
                : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
                  "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]),
@@ -85,23 +86,31 @@ __device__ __forceinline__ void tm_ld16_wait(uint32_t (&r)[16]) {
                :
                : "memory");
 }
-// f(c, 16 columns) for each 16-column group c of a row's 128, the next group's load under way.
-template <typename F>
-__device__ __forceinline__ void for_groups(uint32_t addr, F f) {
-  uint32_t x[16], y[16];
-  tm_ld16_start(addr, x);
+// f(c, W columns) for each W-column part c of a row's 128, the next part's load under way.
+template <int W, typename F>
+__device__ __forceinline__ void for_columns(uint32_t addr, F f) {
+  uint32_t x[W], y[W];
+  auto start = [&](int c, uint32_t *r) {
+#pragma unroll
+    for (int i = 0; i < W; i += 16) tm_ld16_start(addr + W * c + i, r + i);
+  };
+  auto wait = [&](uint32_t *r) {
+#pragma unroll
+    for (int i = 0; i < W; i += 16) tm_ld16_wait(r + i);
+  };
+  start(0, x);
 #pragma unroll 1
-  for (int c = 0; c < 8; c += 2) {
-    tm_ld16_wait(x);
-    tm_ld16_start(addr + 16 * c + 16, y);
+  for (int c = 0; c < 128 / W; c += 2) {
+    wait(x);
+    start(c + 1, y);
     f(c, x);
-    tm_ld16_wait(y);
-    if (c < 6) tm_ld16_start(addr + 16 * c + 32, x);
+    wait(y);
+    if (c + 2 < 128 / W) start(c + 2, x);
     f(c + 1, y);
   }
 }
 
-__device__ __forceinline__ void tm_st8(uint32_t addr, const uint32_t (&r)[8]) {
+__device__ __forceinline__ void tm_st8(uint32_t addr, const uint32_t *r) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(addr),
                "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                : "memory");
@@ -138,9 +147,9 @@ template <int D>
 __global__ void __launch_bounds__(PromptShape<D>::THREADS, 1)
     kv8_prompt_kernel(AttnArgs a, int bf16, int splits) {
   using P = PromptShape<D>;
-  constexpr int NQ = P::NQ, KB = P::KB, WARPS = P::THREADS / 32;
+  constexpr int NQ = P::NQ, WARPS = P::THREADS / 32;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t s_bar[20];
+  __shared__ __align__(8) uint64_t s_bar[24];
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort, s_count[WARPS], s_found[2];
   __shared__ float4 s_meta[8][8];
@@ -149,19 +158,22 @@ __global__ void __launch_bounds__(PromptShape<D>::THREADS, 1)
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t base = (tc::smem_u32(smem_raw) + 1023u) & ~1023u;
   uint8_t *const mem = smem_raw + (base - tc::smem_u32(smem_raw));
-  constexpr uint32_t kAt = NQ * P::TILE, vAt = (NQ + KB) * P::TILE;  // K and V buffers
+  constexpr uint32_t kAt = NQ * P::TILE, vAt = (NQ + P::KB) * P::TILE;  // K and V buffers
   const uint32_t bar = tc::smem_u32(s_bar);
-  const uint32_t k_full = bar, v_full = bar + 16, k_free = bar + 32, v_free = bar + 48;  // [KB]
-  const uint32_t s_full = bar + 64, p_full = bar + 80, pv_done = bar + 96, m_full = bar + 112;  // [2]
-  const uint32_t drain = bar + 128;
+  const uint32_t k_full = bar, k_free = bar + 32;                                        // [KP]
+  const uint32_t v_full = bar + 64, v_free = bar + 80;                                   // [2]
+  const uint32_t s_full = bar + 96, p_full = bar + 112, pv_done = bar + 128, m_full = bar + 144;  // [2]
+  const uint32_t drain = bar + 160;
 
   if (tid == 0) {
     s_abort = 0;
     s_found[0] = -1;
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < 4; ++i) {
       tc::mbar_init(k_full + 8 * i, 128);
-      tc::mbar_init(v_full + 8 * i, 128);
       tc::mbar_init(k_free + 8 * i, 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(v_full + 8 * i, 128);
       tc::mbar_init(v_free + 8 * i, 1);
       tc::mbar_init(s_full + 8 * i, 1);
       tc::mbar_init(p_full + 8 * i, 128);
@@ -355,12 +367,15 @@ __global__ void __launch_bounds__(PromptShape<D>::THREADS, 1)
       }
       // maximum: of a 16-key group's raw scores, then its factor and magnitude
       float top = -INFINITY;
-      for_groups(t_s, [&](int c, const uint32_t (&s)[16]) {
-        const float4 mt = meta[c];
-        float t = -INFINITY;
+      for_columns<P::COLS>(t_s, [&](int c, const uint32_t *s) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) t = fmaxf(t, __uint_as_float(s[i]));
-        if (t > -INFINITY) top = fmaxf(top, fmaf(t, mt.x * qe, mt.y));
+        for (int g = 0; g < P::COLS / 16; ++g) {
+          const float4 mt = meta[c * (P::COLS / 16) + g];
+          float t = -INFINITY;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) t = fmaxf(t, __uint_as_float(s[16 * g + i]));
+          if (t > -INFINITY) top = fmaxf(top, fmaf(t, mt.x * qe, mt.y));
+        }
       });
       // move the running maximum?  (the first tile sets it: O is not there yet)
       if (NQ == 1) {  // the other group's last tile has decided
@@ -401,20 +416,25 @@ __global__ void __launch_bounds__(PromptShape<D>::THREADS, 1)
       }
       if (NQ == 1) tc::mbar_arrive(m_full + 8 * wg);
       const float m0 = m == -INFINITY ? 0.f : m;
-      for_groups(t_s, [&](int c, const uint32_t (&s)[16]) {
-        const float4 mt = meta[c];
-        const float f = mt.x * qe, off = mt.y - m0;
-        float sum = 0.f;
-        uint32_t p[8];
+      for_columns<P::COLS>(t_s, [&](int c, const uint32_t *s) {
+        uint32_t p[P::COLS / 2];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float x0 = ex2_approx(fmaf(__uint_as_float(s[2 * i]), f, off));
-          const float x1 = ex2_approx(fmaf(__uint_as_float(s[2 * i + 1]), f, off));
-          sum += x0 + x1;
-          p[i] = F16::from_f32x2(x0, x1);
+        for (int g = 0; g < P::COLS / 16; ++g) {
+          const float4 mt = meta[c * (P::COLS / 16) + g];
+          const float f = mt.x * qe, off = mt.y - m0;
+          float sum[2] = {0.f, 0.f};
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float x0 = ex2_approx(fmaf(__uint_as_float(s[16 * g + 2 * i]), f, off));
+            const float x1 = ex2_approx(fmaf(__uint_as_float(s[16 * g + 2 * i + 1]), f, off));
+            sum[0] += x0;
+            sum[1] += x1;
+            p[8 * g + i] = F16::from_f32x2(x0, x1);
+          }
+          l = fmaf(sum[0] + sum[1], mt.z, l);
         }
-        l = fmaf(sum, mt.z, l);
-        tm_st8(t_s + 8 * c, p);
+#pragma unroll
+        for (int i = 0; i < P::COLS / 2; i += 8) tm_st8(t_s + c * (P::COLS / 2) + i, p + i);
       });
       tm_st_wait();
       tc::tc_fence_before();
@@ -475,136 +495,168 @@ __global__ void __launch_bounds__(PromptShape<D>::THREADS, 1)
   } else if (warp < 8 + P::CW) {
     // ======================================================================== codes -> operands
     const int w = warp & 3;
-    // K: this warp's 32 keys; a load covers 512 bytes of consecutive codes
-    constexpr int LPR = D / 16, RPL = 32 / LPR, KL = 32 / RPL;  // lanes a row, rows a load, loads
-    // V: 64 keys by 16 VW elements a unit; lane (tg, dg) holds 8 tokens' VW words
+    // K: this warp's 32 keys; a load covers 8 keys by 64 elements (an atom: 128 bytes of fp16 a key)
+    constexpr int ATOMS = D / 64;
+    // V: 64 keys by 16 VW elements a unit; lane (tg, dg) holds the VW words of 8 tokens (group tg)
     constexpr int VU = D / (16 * P::VW) * 2 / 4;  // units a warp
-    const int tg = lane & 7, dg = lane >> 3;
+    // of elements dg.  Eight lanes load two tokens' 64 bytes; for each 16-byte store of eight tokens
+    // they hold the token groups t and t + 4 and the rows 4k + (e ^ dg): the swizzled chunks
+    // {t, t + 4} ^ {e ^ dg} are eight different ones.
+    const int tg = (lane >> 2 & 1) * 4 + (lane >> 3), dg = lane & 3;
+    const uint32_t pair0 = dg | (4 + dg) << 4 | (dg ^ 1) << 8 | (4 + (dg ^ 1)) << 12;  // bytes dg, dg ^ 1
+    const uint32_t pair1 = (dg ^ 2) | (4 + (dg ^ 2)) << 4 | (dg ^ 3) << 8 | (4 + (dg ^ 3)) << 12;
     // A page's codes beyond the sequence's end are loaded as they are, and page 0 in the place of one
     // that is not there: their scores are hidden, so their weights are 0.  Nothing is selected after
     // a load, which would wait for it.
-    auto load_k = [&](uint4 (&kr)[KL], int j, int raw) {
+    const int8_t *ksrc[2];  // the keys of this warp's two groups in the next tile
+    auto find_k = [&](int j, int raw) {
       const int pages = check_page(B, raw, a.hdr);
 #pragma unroll
       for (int g = 0; g < 2; ++g) {
         const int pg = max(__shfl_sync(~0u, pages, 2 * w + g), 0);
         const int in_page = (key0 + j * kKeys + 32 * w + 16 * g) & (B.page - 1);
-        const uint4 *src = reinterpret_cast<const uint4 *>(
-            a.k + (((int64_t)pg * a.kv_heads + h) * B.page + in_page) * D) + lane;
-#pragma unroll
-        for (int i = 0; i < KL / 2; ++i) kr[g * (KL / 2) + i] = __ldg(src + i * 32);
+        ksrc[g] = a.k + (((int64_t)pg * a.kv_heads + h) * B.page + in_page + (lane >> 2)) * D + (lane & 3) * 16;
       }
     };
-    auto store_k = [&](const uint4 (&kr)[KL], int j) {
+    auto load_k = [&](uint4 (&kr)[4], int atom) {
 #pragma unroll
-      for (int i = 0; i < KL; ++i) {
-        const int row = 32 * w + i * RPL + lane / LPR, mch = lane % LPR;
+      for (int i = 0; i < 4; ++i)
+        kr[i] = __ldg(reinterpret_cast<const uint4 *>(ksrc[i >> 1] + (i & 1) * 8 * D + atom * 64));
+    };
+    auto store_k = [&](const uint4 (&kr)[4], uint8_t *atom) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int row = 32 * w + 8 * i + (lane >> 2), c = 2 * (lane & 3);
         const uint32_t u[4] = {kr[i].x ^ 0x80808080u, kr[i].y ^ 0x80808080u, kr[i].z ^ 0x80808080u,
                                kr[i].w ^ 0x80808080u};
-        const uint4 lo = make_uint4(codes_f16(u[0], kPickLo), codes_f16(u[0], kPickHi),
-                                    codes_f16(u[1], kPickLo), codes_f16(u[1], kPickHi));
-        const uint4 hi = make_uint4(codes_f16(u[2], kPickLo), codes_f16(u[2], kPickHi),
-                                    codes_f16(u[3], kPickLo), codes_f16(u[3], kPickHi));
-        // 8 lanes of a row: the second atom's four store their odd chunk first, so that the
-        // eight 16-byte stores of a phase meet eight bank groups
-        const bool odd = (mch >> 2) & 1;
-        uint8_t *atom = mem + kAt + (j % KB) * P::TILE + (mch >> 2) * (kKeys * 128);
-        const int c = 2 * (mch & 3);
-        *reinterpret_cast<uint4 *>(atom + tc::sw128(row, c + odd)) = odd ? hi : lo;
-        *reinterpret_cast<uint4 *>(atom + tc::sw128(row, c + !odd)) = odd ? lo : hi;
+        // 8 lanes: two rows, an even and an odd one, whose four chunks fall into 8 bank groups
+        *reinterpret_cast<uint4 *>(atom + tc::sw128(row, c)) =
+            make_uint4(codes_f16(u[0], kPickLo), codes_f16(u[0], kPickHi), codes_f16(u[1], kPickLo), codes_f16(u[1], kPickHi));
+        *reinterpret_cast<uint4 *>(atom + tc::sw128(row, c + 1)) =
+            make_uint4(codes_f16(u[2], kPickLo), codes_f16(u[2], kPickHi), codes_f16(u[3], kPickLo), codes_f16(u[3], kPickHi));
       }
     };
-    auto load_v = [&](uint32_t (&vr)[VU][8][P::VW], int j, int raw) {
+    const int8_t *vsrc[VU];
+    auto find_v = [&](int j, int raw) {
       const int pages = check_page(B, raw, a.hdr);
 #pragma unroll
       for (int u = 0; u < VU; ++u) {
         const int unit = w * VU + u, half = unit & 1, d0 = (unit >> 1) * 16 * P::VW + dg * 4 * P::VW;
         const int pg = max(__shfl_sync(~0u, pages, half * 4 + (tg >> 1)), 0);
         const int in_page = (key0 + j * kKeys + half * 64 + tg * 8) & (B.page - 1);
-        const int8_t *src = a.v + (((int64_t)pg * a.kv_heads + h) * B.page + in_page) * D + d0;
+        vsrc[u] = a.v + (((int64_t)pg * a.kv_heads + h) * B.page + in_page) * D + d0;
+      }
+    };
+    auto load_v = [&](uint32_t (&vr)[8][P::VW], const int8_t *src) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          if (P::VW == 4) {
-            const uint4 x = __ldg(reinterpret_cast<const uint4 *>(src + i * D));
-            vr[u][i][0] = x.x, vr[u][i][1] = x.y, vr[u][i][P::VW - 2] = x.z, vr[u][i][P::VW - 1] = x.w;
-          } else {
-            const uint2 x = __ldg(reinterpret_cast<const uint2 *>(src + i * D));
-            vr[u][i][0] = x.x, vr[u][i][1] = x.y;
-          }
+      for (int i = 0; i < 8; ++i) {
+        if (P::VW == 4) {
+          const uint4 x = __ldg(reinterpret_cast<const uint4 *>(src + i * D));
+          vr[i][0] = x.x, vr[i][1] = x.y, vr[i][P::VW - 2] = x.z, vr[i][P::VW - 1] = x.w;
+        } else {
+          const uint2 x = __ldg(reinterpret_cast<const uint2 *>(src + i * D));
+          vr[i][0] = x.x, vr[i][1] = x.y;
         }
       }
     };
-    auto store_v = [&](const uint32_t (&vr)[VU][8][P::VW], int j) {
+    auto store_v = [&](const uint32_t (&vr)[8][P::VW], int u, uint8_t *buf) {
+      const int unit = w * VU + u, half = unit & 1, d0 = (unit >> 1) * 16 * P::VW + dg * 4 * P::VW;
+      uint8_t *atom = buf + half * (D * 128);
 #pragma unroll
-      for (int u = 0; u < VU; ++u) {
-        const int unit = w * VU + u, half = unit & 1, d0 = (unit >> 1) * 16 * P::VW + dg * 4 * P::VW;
-        uint8_t *atom = mem + vAt + (j % KB) * P::TILE + half * (D * 128);
+      for (int k = 0; k < P::VW; ++k) {
+        uint32_t z[4][2];
 #pragma unroll
-        for (int k = 0; k < P::VW; ++k) {
-          uint32_t z[4][2];
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t x = vr[2 * i][k] ^ 0x80808080u, y = vr[2 * i + 1][k] ^ 0x80808080u;
+          z[i][0] = __byte_perm(x, y, pair0);
+          z[i][1] = __byte_perm(x, y, pair1);
+        }
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint32_t x = vr[u][2 * i][k] ^ 0x80808080u, y = vr[u][2 * i + 1][k] ^ 0x80808080u;
-            z[i][0] = __byte_perm(x, y, 0x5140);
-            z[i][1] = __byte_perm(x, y, 0x7362);
-          }
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const uint32_t pick = e & 1 ? kPickHi : kPickLo;
-            *reinterpret_cast<uint4 *>(atom + tc::sw128(d0 + 4 * k + e, tg)) =
-                make_uint4(codes_f16(z[0][e >> 1], pick), codes_f16(z[1][e >> 1], pick),
-                           codes_f16(z[2][e >> 1], pick), codes_f16(z[3][e >> 1], pick));
-          }
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t pick = e & 1 ? kPickHi : kPickLo;
+          *reinterpret_cast<uint4 *>(atom + tc::sw128(d0 + 4 * k + (e ^ dg), tg)) =
+              make_uint4(codes_f16(z[0][e >> 1], pick), codes_f16(z[1][e >> 1], pick),
+                         codes_f16(z[2][e >> 1], pick), codes_f16(z[3][e >> 1], pick));
         }
       }
     };
-    // buffer j % KB is free once the product that read its last contents is done
-    auto free_wait = [&](uint32_t bars, int j) {
-      return j < KB || wait_warp(bars + 8 * (j % KB), (j / KB - 1) & 1, abort_flag, err);
+    // A buffer's n-th contents may be written once the product that read the last ones is done.
+    auto free_wait = [&](uint32_t b, int n) {
+      return n == 0 || wait_warp(b, (n - 1) & 1, abort_flag, err);
     };
-    auto publish = [&](uint32_t bars, int j) {
-      tc::fence_proxy_async();
-      tc::mbar_arrive(bars + 8 * (j % KB));
-    };
-    int page = page_of(1, lane & 7);
+    // The proxy fence between these stores and the products is the issuing warp's, after its wait: here
+    // it would wait for the loads of the next codes too (a half of V took 2,000 cycles instead of 500).
+    auto publish = [&](uint32_t b) { tc::mbar_arrive(b); };
     const int page0 = page_of(0, lane & 7);
-    if constexpr (P::CW == 4) {
-      uint4 kr[KL];
+    int page = page_of(1, lane & 7);
+    if constexpr (NQ == 2) {
+      // two buffers of whole tiles, the same warps for keys and values
+      uint4 kr[ATOMS][4];
       uint32_t vr[VU][8][P::VW];
-      load_k(kr, 0, page0);
-      load_v(vr, 0, page0);
+      find_k(0, page0);
+      find_v(0, page0);
+#pragma unroll
+      for (int i = 0; i < ATOMS; ++i) load_k(kr[i], i);
+#pragma unroll
+      for (int u = 0; u < VU; ++u) load_v(vr[u], vsrc[u]);
       for (int j = 0; j < tiles; ++j) {
-        const int next = page_of(j + 2, lane & 7);
-        if (!free_wait(k_free, j)) break;
-        store_k(kr, j);
-        publish(k_full, j);
-        load_k(kr, j + 1, page);
-        if (!free_wait(v_free, j)) break;
-        store_v(vr, j);
-        publish(v_full, j);
-        load_v(vr, j + 1, page);
+        const int next = page_of(j + 2, lane & 7), b = j & 1;
+        find_k(j + 1, page);
+        find_v(j + 1, page);
+        if (!free_wait(k_free + 8 * b, j >> 1)) break;
+#pragma unroll
+        for (int i = 0; i < ATOMS; ++i) {
+          store_k(kr[i], mem + kAt + b * P::TILE + i * (kKeys * 128));
+          load_k(kr[i], i);
+        }
+        publish(k_full + 8 * b);
+        if (!free_wait(v_free + 8 * b, j >> 1)) break;
+#pragma unroll
+        for (int u = 0; u < VU; ++u) {
+          store_v(vr[u], u, mem + vAt + b * P::TILE);
+          load_v(vr[u], vsrc[u]);
+        }
+        publish(v_full + 8 * b);
         page = next;
       }
     } else if (warp < 12) {
-      uint4 kr[KL];
-      load_k(kr, 0, page0);
-      for (int j = 0; j < tiles; ++j) {
+      // one buffer of K, whose four atoms come free and are filled one after the other; two atoms'
+      // codes are under way
+      uint4 kr[2][4];
+      find_k(0, page0);
+      load_k(kr[0], 0);
+      load_k(kr[1], 1);
+      bool ok = true;
+      for (int j = 0; j < tiles && ok; ++j) {
         const int next = page_of(j + 2, lane & 7);
-        if (!free_wait(k_free, j)) break;
-        store_k(kr, j);
-        publish(k_full, j);
-        load_k(kr, j + 1, page);
+#pragma unroll
+        for (int i = 0; i < ATOMS; ++i) {
+          ok = ok && free_wait(k_free + 8 * i, j);
+          if (!ok) break;
+          store_k(kr[i & 1], mem + kAt + i * (kKeys * 128));
+          publish(k_full + 8 * i);
+          if (i == ATOMS - 2) find_k(j + 1, page);
+          load_k(kr[i & 1], (i + 2) % ATOMS);
+        }
         page = next;
       }
     } else {
-      uint32_t vr[VU][8][P::VW];
-      load_v(vr, 0, page0);
-      for (int j = 0; j < tiles; ++j) {
+      // one buffer of V, in halves of 64 keys; the other half's codes are under way
+      uint32_t vr[8][P::VW];
+      find_v(0, page0);
+      load_v(vr, vsrc[0]);
+      bool ok = true;
+      for (int j = 0; j < tiles && ok; ++j) {
         const int next = page_of(j + 2, lane & 7);
-        if (!free_wait(v_free, j)) break;
-        store_v(vr, j);
-        publish(v_full, j);
-        load_v(vr, j + 1, page);
+#pragma unroll
+        for (int u = 0; u < VU; ++u) {
+          ok = ok && free_wait(v_free + 8 * u, j);
+          if (!ok) break;
+          store_v(vr, u, mem + vAt);
+          publish(v_full + 8 * u);
+          if (u == VU - 1) find_v(j + 1, page);
+          load_v(vr, vsrc[(u + 1) % VU]);
+        }
         page = next;
       }
     }
@@ -613,69 +665,89 @@ __global__ void __launch_bounds__(PromptShape<D>::THREADS, 1)
     asm volatile("bar.sync 1, 288;" ::: "memory");
     bool ok = true;
     auto wait = [&](uint32_t b, int phase) { ok = ok && wait_warp(b, phase & 1, abort_flag, err); };
-    auto issue_qk = [&](int j, int q, int slot) {  // S slot = Q(q) K(j)^T
+    auto wait_codes = [&](uint32_t b, int phase) {
+      wait(b, phase);
+      tc::fence_proxy_async();  // the converting warps' stores, for the products that read them
+    };
+    // S slot = Q(q) K^T over the elements [64 first, 64 last) of a K buffer
+    auto qk = [&](uint32_t sk, int q, int slot, int first, int last) {
       if (!ok) return;
       tc::tc_fence_after();
-      const uint32_t sq = base + q * P::TILE, sk = base + kAt + (j % KB) * P::TILE;
+      const uint32_t sq = base + q * P::TILE;
 #pragma unroll
-      for (int ks = 0; ks < D / 16; ++ks) {
+      for (int ks = 4 * first; ks < 4 * last; ++ks) {
         const uint32_t off = (ks >> 2) * (kKeys * 128) + (ks & 3) * 32;
         tc::mma_bf16_warp(tmem + 128 * slot, tc::desc_k128_sw128(sq + off), tc::desc_k128_sw128(sk + off),
                           idesc_f16(kKeys), ks > 0);
       }
-      tc::mma_commit_warp(s_full + 8 * slot);
     };
-    auto issue_pv = [&](int j, int q, int slot) {  // O(q) += P slot V(j)
+    // O(q) += P slot V over the keys [64 first, 64 last) of a V buffer
+    auto pv = [&](uint32_t sv, int q, int slot, int first, int last, bool fresh) {
       if (!ok) return;
       tc::tc_fence_after();
-      const uint32_t sv = base + vAt + (j % KB) * P::TILE;
 #pragma unroll
-      for (int ks = 0; ks < kKeys / 16; ++ks) {
+      for (int ks = 4 * first; ks < 4 * last; ++ks) {
         const uint32_t off = (ks >> 2) * (D * 128) + (ks & 3) * 32;
         tc::mma_bf16_ts_warp(tmem + 256 + q * D, tmem + 128 * slot + 8 * ks, tc::desc_k128_sw128(sv + off),
-                             idesc_f16(D), j > 0 || ks > 0);
+                             idesc_f16(D), !fresh || ks > 0);
       }
-      tc::mma_commit_warp(pv_done + 8 * q);
     };
-    if (NQ == 2) {
+    auto commit = [&](uint32_t b) {
+      if (ok) tc::mma_commit_warp(b);
+    };
+    if constexpr (NQ == 2) {
       // the two row tiles take turns: while one's weights are computed the other's products run
       if (tiles > 0) {
-        wait(k_full, 0);
-        for (int q = 0; q < nq; ++q) issue_qk(0, q, q);
-        if (ok) tc::mma_commit_warp(k_free);
+        wait_codes(k_full, 0);
+        for (int q = 0; q < nq; ++q) {
+          qk(base + kAt, q, q, 0, D / 64);
+          commit(s_full + 8 * q);
+        }
+        commit(k_free);
       }
       for (int j = 0; j < tiles && ok; ++j) {
-        wait(v_full + 8 * (j % KB), j / KB);
+        const int b = j & 1;
+        wait_codes(v_full + 8 * b, j >> 1);
         for (int q = 0; q < nq; ++q) {
           wait(p_full + 8 * q, j);
-          issue_pv(j, q, q);
-          if (q == nq - 1 && ok) tc::mma_commit_warp(v_free + 8 * (j % KB));
+          pv(base + vAt + b * P::TILE, q, q, 0, 2, j == 0);
+          commit(pv_done + 8 * q);
+          if (q == nq - 1) commit(v_free + 8 * b);
           if (j + 1 < tiles) {
-            if (q == 0) wait(k_full + 8 * ((j + 1) % KB), (j + 1) / KB);
+            if (q == 0) wait_codes(k_full + 8 * (b ^ 1), (j + 1) >> 1);
             wait(pv_done + 8 * q, j);  // S takes the columns of P
-            issue_qk(j + 1, q, q);
-            if (q == nq - 1 && ok) tc::mma_commit_warp(k_free + 8 * ((j + 1) % KB));
+            qk(base + kAt + (b ^ 1) * P::TILE, q, q, 0, D / 64);
+            commit(s_full + 8 * q);
+            if (q == nq - 1) commit(k_free + 8 * (b ^ 1));
           }
         }
       }
     } else {
-      // the next tile's scores are computed under this one's softmax, in the other slot
-      if (tiles > 0) {
-        wait(k_full, 0);
-        issue_qk(0, 0, 0);
-        if (ok) tc::mma_commit_warp(k_free);
-      }
+      // the next tile's scores are computed under this one's softmax, in the other slot; K's atoms
+      // and V's halves are given back as soon as they have been read
+      auto scores = [&](int j) {
+#pragma unroll
+        for (int i = 0; i < D / 64; ++i) {
+          wait_codes(k_full + 8 * i, j);
+          qk(base + kAt, 0, j & 1, i, i + 1);
+          commit(k_free + 8 * i);
+        }
+        commit(s_full + 8 * (j & 1));
+      };
+      if (tiles > 0) scores(0);
       for (int j = 0; j < tiles && ok; ++j) {
         if (j + 1 < tiles) {
           if (j > 0) wait(pv_done, j - 1);  // that slot's weights have been used
-          wait(k_full, j + 1);
-          issue_qk(j + 1, 0, (j + 1) & 1);
-          if (ok) tc::mma_commit_warp(k_free);
+          scores(j + 1);
         }
-        wait(v_full, j);
         wait(p_full + 8 * (j & 1), j >> 1);
-        issue_pv(j, 0, j & 1);
-        if (ok) tc::mma_commit_warp(v_free);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          wait_codes(v_full + 8 * u, j);
+          pv(base + vAt, 0, j & 1, u, u + 1, j == 0);
+          commit(v_free + 8 * u);
+        }
+        commit(pv_done);
       }
     }
     // nothing of this warp's products is in flight when the tensor memory is given back
