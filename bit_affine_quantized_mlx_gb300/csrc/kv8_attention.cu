@@ -658,16 +658,25 @@ static cudaError_t launch_decode_dim(const AttnArgs &a, const DecodePlan &p, int
   return cudaErrorInvalidValue;
 }
 
-// Rows of a sequence and key/value head from which the tcgen05 form runs.
-constexpr int kPromptRows = 33;
+// Rows of a sequence and key/value head from which the tcgen05 form runs.  Measured with both forms
+// (us, split / tcgen05): 32 sequences of 4096 keys, 8 heads of 128: 16 rows 76 / 137, 32 rows
+// 147 / 138, 48 rows 264 / 138; 4 heads of 64: 16 rows 32 / 54, 32 rows 52 / 55, 64 rows 87 / 55;
+// 2 heads of 256: 32 rows 75 / 66, 64 rows 124 / 67; one sequence of 32768 keys, 8 heads of 128:
+// 32 rows 41 / 45, 48 rows 64 / 45.  With heads of 256 and so few sequences that the tcgen05 form has to
+// split the keys, its parts' outputs (128 rows of 256 each) cost more than reading the codes again:
+// one sequence, 2 heads, 32768 keys: 64 rows 40 / 60, 96 rows 56 / 61, 128 rows 62 / 62.
+static int prompt_rows(const lily_kv8_cache &C, const lily_kv8_batch &b) {
+  const int sms = sm_count() > 0 ? sm_count() : 152;
+  return C.head_dim == 256 && (int64_t)b.batch * C.kv_heads * 4 <= sms ? 97 : 33;
+}
 static bool prompt_form(const lily_kv8_cache &C, const lily_kv8_batch &b, int q_heads) {
-  return (int64_t)b.max_q * (q_heads / C.kv_heads) >= kPromptRows;
+  return (int64_t)b.max_q * (q_heads / C.kv_heads) >= prompt_rows(C, b);
 }
 
 size_t kv8_attention_ws_bytes(const lily_kv8_cache &C, const lily_kv8_batch &b, int T, int q_heads) {
   if (!prompt_form(C, b, q_heads)) return decode_plan(C, b, T, q_heads).total;
   lily_kv8_batch fewer = b;  // the split form's largest calls, so that the space serves them too
-  fewer.max_q = std::max(1, (kPromptRows - 1) / (q_heads / C.kv_heads));
+  fewer.max_q = std::max(1, 96 / (q_heads / C.kv_heads));
   return std::max(decode_plan(C, fewer, T, q_heads).total, prompt_plan(C, b, T, q_heads).total);
 }
 
