@@ -14,9 +14,9 @@
 // follows them.
 //
 // Block.  Four warps take the tiles' keys in turns of 4096 bytes of keys and of values each (16 to
-// 64 tokens).  Each warp keeps its own ring of three such turns in shared memory, filled by 16-byte
-// cp.async of its own, so there is no barrier in the loop; two blocks an SM keep up to 128 KB in
-// flight.  The codes become fp16 exactly in registers (q + 1152 - 1152, see codes_f16) and meet
+// 64 tokens).  Each warp keeps its own ring of two such turns in shared memory, filled by 16-byte
+// cp.async of its own, so there is no barrier in the loop; three blocks an SM (head_dim 256: two) keep
+// 64 to 96 KB in flight (a third turn in the ring gained nothing).  The codes become fp16 exactly in registers (q + 1152 - 1152, see codes_f16) and meet
 // their products as mma.sync m16n8k16 with the KEYS (then the head's elements) as the 16 rows and the
 // queries as the 8 columns: at 8 rows a head nothing is padded, and at this shape the tensor pipe is
 // far from its limit (the codes arrive at 22 bytes a clock and SM).
@@ -40,7 +40,7 @@
 
 namespace lq4 {
 
-constexpr int kDecThreads = 128, kDecWarps = 4, kDecStages = 3;
+constexpr int kDecThreads = 128, kDecWarps = 4, kDecStages = 2;
 constexpr int kTurnBytes = 4096;  // of keys, and of values, a warp and turn
 
 __device__ __forceinline__ float ex2(float x) {
@@ -83,8 +83,18 @@ __device__ __forceinline__ RowOf row_of(const Seq &s, int rr, int h, int group) 
   return RowOf{i < s.n ? s.row0 + i : -1, h * group + rr - i * group};
 }
 
+// Bytes of a warp's ring, which holds its outputs (8 NT rows of D + 2 floats) when the warps are joined.
+constexpr int ring_bytes(int D, int NT) {
+  const int ring = kDecStages * 2 * kTurnBytes, out = 8 * NT * (D + 2) * 4;
+  return ring > out ? ring : (out + 127) / 128 * 128;
+}
+
+// Blocks an SM: three where 168 registers hold a tile of 8 rows (64 sequences up to 32k tokens of 8 heads
+// of 128: 383 us with two, 352 with three), else two.
+constexpr int decode_blocks(int D, int NT) { return D <= 128 && NT == 1 ? 3 : 2; }
+
 template <int D, int NT>
-__global__ void __launch_bounds__(kDecThreads, 2) kv8_decode_kernel(AttnArgs a, int bf16) {
+__global__ void __launch_bounds__(kDecThreads, decode_blocks(D, NT)) kv8_decode_kernel(AttnArgs a, int bf16) {
   constexpr int RT = 8 * NT;             // rows of a tile
   constexpr int WS = kTurnBytes / D;     // tokens of a turn
   constexpr int NG = WS / 16;            // 16-token groups of a turn
@@ -92,7 +102,7 @@ __global__ void __launch_bounds__(kDecThreads, 2) kv8_decode_kernel(AttnArgs a, 
   constexpr int MT = D / 16;
   constexpr int QS = D * 2 + 16;         // bytes between rows of q
   constexpr bool QREG = D * NT <= 256;   // q's operands stay in registers
-  constexpr int RING = kDecStages * 2 * kTurnBytes;
+  constexpr int RING = ring_bytes(D, NT);
   extern __shared__ __align__(128) uint8_t smem[];
   uint8_t *s_q = smem + kDecWarps * RING;
   float *s_meta = reinterpret_cast<float *>(s_q + RT * QS);  // [warp][stage][2][NG]
@@ -531,19 +541,33 @@ __global__ void __launch_bounds__(kJoinThreads) kv8_join_kernel(AttnArgs a, int 
     c = s_job;
     if (c < 0) return;
   }
-  const int4 j0 = a.jobs[2 * c];
+  const int4 j0 = a.jobs[2 * c], j1 = a.jobs[2 * c + 1];
   if (j0.x < 0) return;
-  const int4 j1 = a.jobs[2 * c + 1];
   const RowOf ro = row_of(Seq{j0.x, j0.y, 0}, j0.w * RT + r, j0.z, a.group);
   if (ro.row < 0) return;
   const int parts = j1.y - c + 1;  // at most the first launch's blocks, kJoinMost
   auto slot = [&](int i) { return i == 0 ? j1.x : 2 * (c + i); };
 
+  // the first parts' outputs are under way while their weights are found
+  constexpr int COLS = D / 4, GROUPS = kJoinThreads / COLS, AHEAD = 8;
+  const int col = tid % COLS, grp = tid / COLS;
+  auto part = [&](int i) {
+    return *reinterpret_cast<const float4 *>(a.part + ((int64_t)slot(i) * RT + r) * D + col * 4);
+  };
+  float4 first[AHEAD];
+#pragma unroll
+  for (int k = 0; k < AHEAD; ++k) {
+    first[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (grp + k * GROUPS < parts) first[k] = part(grp + k * GROUPS);
+  }
+  constexpr int MINE = kJoinMost / kJoinThreads;
+  float2 ml[MINE];  // parts tid, tid + kJoinThreads ...
   float top = -INFINITY;
-  for (int i = tid; i < parts; i += kJoinThreads) {
-    const float m = a.ml[(int64_t)slot(i) * RT + r].x;
-    s_w[i] = m;
-    top = fmaxf(top, m);
+#pragma unroll
+  for (int k = 0; k < MINE; ++k) {
+    const int i = tid + k * kJoinThreads;
+    ml[k] = i < parts ? a.ml[(int64_t)slot(i) * RT + r] : make_float2(-INFINITY, 0.f);
+    top = fmaxf(top, ml[k].x);
   }
 #pragma unroll
   for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
@@ -552,10 +576,11 @@ __global__ void __launch_bounds__(kJoinThreads) kv8_join_kernel(AttnArgs a, int 
 #pragma unroll
   for (int w = 0; w < WARPS; ++w) top = fmaxf(top, s_red[w]);
   float den = 0.f;
-  for (int i = tid; i < parts; i += kJoinThreads) {
-    const float f = s_w[i] == -INFINITY ? 1.f : ex2(s_w[i] - top);  // sum and output 0, or NaN
-    s_w[i] = f;
-    den += f * a.ml[(int64_t)slot(i) * RT + r].y;
+#pragma unroll
+  for (int k = 0; k < MINE; ++k) {
+    const float f = ml[k].x == -INFINITY ? 1.f : ex2(ml[k].x - top);  // sum and output 0, or NaN
+    s_w[tid + k * kJoinThreads] = f;
+    den = fmaf(f, ml[k].y, den);
   }
 #pragma unroll
   for (int o = 16; o; o >>= 1) den += __shfl_xor_sync(~0u, den, o);
@@ -565,18 +590,18 @@ __global__ void __launch_bounds__(kJoinThreads) kv8_join_kernel(AttnArgs a, int 
 #pragma unroll
   for (int w = 0; w < WARPS; ++w) den += s_den[w];
 
-  constexpr int COLS = D / 4, GROUPS = kJoinThreads / COLS;
-  const int col = tid % COLS, grp = tid / COLS;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-  for (int i = grp; i < parts; i += GROUPS) {
-    const float4 u = *reinterpret_cast<const float4 *>(a.part + ((int64_t)slot(i) * RT + r) * D + col * 4);
-    const float w = s_w[i];
+  auto add = [&](const float4 &u, float w) {
     acc.x = fmaf(u.x, w, acc.x);
     acc.y = fmaf(u.y, w, acc.y);
     acc.z = fmaf(u.z, w, acc.z);
     acc.w = fmaf(u.w, w, acc.w);
-  }
+  };
+#pragma unroll
+  for (int k = 0; k < AHEAD; ++k)
+    if (grp + k * GROUPS < parts) add(first[k], s_w[grp + k * GROUPS]);
+#pragma unroll 8
+  for (int i = grp + AHEAD * GROUPS; i < parts; i += GROUPS) add(part(i), s_w[i]);
   reinterpret_cast<float4 *>(s_o)[tid] = acc;
   __syncthreads();
   if (grp == 0) {
@@ -617,15 +642,15 @@ static DecodePlan decode_plan(const lily_kv8_cache &C, const lily_kv8_batch &b, 
   const int64_t items = std::min<int64_t>(b.batch, T) * ((rows + RT - 1) / RT) * C.kv_heads;
   const int64_t tiles = std::max<int64_t>(1, ((int64_t)b.max_kv + 16 + tile - 1) / tile);
   if (items > INT32_MAX / tiles) return p;  // total 0: the tiles have to be countable in 31 bits
-  p.grid = (int)std::max<int64_t>(1, std::min<int64_t>(std::min(2 * sms, kJoinMost), items * tiles));
+  p.grid = (int)std::max<int64_t>(1, std::min<int64_t>(std::min(decode_blocks(D, p.nt) * sms, kJoinMost), items * tiles));
   // Few items have many parts each: a large block reads a row's parts together (262,144 tokens, 152
-  // parts: 12 us with 256 threads, 8 with 512).  Many items have two or three: small blocks start
+  // parts: 12 us with 256 threads, 8 with 512).  Fewer: small blocks start
   // faster (64 sequences, 512 items: 6 us with 256 threads, 10 with 512).
-  p.join = tiles == 1 ? 0 : p.grid / items >= 8 ? kJoinMost : 128;
+  p.join = tiles == 1 ? 0 : p.grid / items >= 32 ? kJoinMost : 128;
   p.items = (int)std::min<int64_t>(items, p.grid);
   p.rows = (int)std::min<int64_t>(RT, rows);
   const int ng = kTurnBytes / D / 16;
-  p.smem = kDecWarps * kDecStages * 2 * kTurnBytes + RT * (D * 2 + 16) +
+  p.smem = kDecWarps * ring_bytes(D, p.nt) + RT * (D * 2 + 16) +
            4 * (kDecWarps * kDecStages * 2 * ng + RT + 2 * kDecWarps * RT + 4 + b.batch + 1);
   size_t off = kAlign;
   p.off_jobs = off;

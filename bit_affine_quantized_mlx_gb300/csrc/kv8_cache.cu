@@ -175,13 +175,14 @@ __global__ void __launch_bounds__(TEAM *TEAMS) kv8_append_kernel(CacheArgs a) {
 }
 
 // ----------------------------------------------------------------------------- read
-// A warp takes 8 tokens: lanes 0-7 find their sequences and pages together, then the warp walks the
+// A warp takes up to 8 tokens: as many lanes find their sequences and pages together, then it walks the
 // tokens' heads, D / 16 lanes a head and 16 codes a lane, four loads of codes in flight.  Bound by
 // memory (1 byte in, 2 or 4 out an element).
-constexpr int kReadThreads = 256, kReadTokens = 8, kReadAhead = 4;
+constexpr int kReadThreads = 256, kReadAhead = 4;
 
 template <int DT>
 __global__ void __launch_bounds__(kReadThreads) kv8_read_kernel(CacheArgs a) {
+  const int kReadTokens = a.chunk;
   pdl_wait();
   const Batch &B = a.B;
   const int lane = threadIdx.x & 31;
@@ -338,7 +339,11 @@ int launch_kv8_read(const lily_kv8_cache &C, const lily_kv8_batch &b, int T, int
   a.ts[1] = v.ts;
   a.hs[0] = k.hs;
   a.hs[1] = v.hs;
-  const int per = kReadThreads / 32 * kReadTokens;
+  // Tokens of a warp: 8 where that leaves about 8 warps an SM, fewer where there are fewer tokens (16
+  // sequences of a page: 9 us with 8, 5 with 1).
+  const int sms = sm_count() > 0 ? sm_count() : 1;
+  a.chunk = std::max(1, std::min(8, T / (4 * sms)));
+  const int per = kReadThreads / 32 * a.chunk;
   const dim3 grid((T + per - 1) / per, 2), block(kReadThreads);
   if (dtype == LILY_BF16) return status_of(launch_pdl(kv8_read_kernel<LILY_BF16>, grid, block, 0, st, a));
   if (dtype == LILY_F16) return status_of(launch_pdl(kv8_read_kernel<LILY_F16>, grid, block, 0, st, a));

@@ -9,6 +9,8 @@
 
 namespace lq4 {
 
+// Wait for the kernel before this one on the stream.  (Letting the next kernel's blocks in early was
+// tried: they took places from this one's and gained nothing.)
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // ----------------------------------------------------------------------------- 16-bit types
