@@ -24,6 +24,7 @@ from __future__ import annotations
 
 import ctypes as C
 import os
+import struct
 from typing import Optional
 
 import numpy as np
@@ -132,7 +133,8 @@ def load(path: Optional[str] = None):
                                      vp, vp, sz, vp]
     L.lily_kv8_attention_workspace_bytes.argtypes = [cache, batch, i32, i32]
     L.lily_kv8_attention_workspace_bytes.restype = sz
-    for f in ("lily_rope_turns", "lily_qk_norm_rope", "lily_kv8_append", "lily_kv8_read",
+    L.lily_q4_call.argtypes = [i32, C.c_char_p]
+    for f in ("lily_q4_call", "lily_rope_turns", "lily_qk_norm_rope", "lily_kv8_append", "lily_kv8_read",
               "lily_kv8_attention",
               "lily_q4_moe_decode", "lily_q4_moe_prefill", "lily_q4_gemv_argmax",
               "lily_q4_workspace_init", "lily_q4_workspace_status", "lily_q4_pack",
@@ -398,14 +400,19 @@ def lily_q4_unpack(w: np.ndarray, N: int, K: int) -> np.ndarray:
 _DTYPES = {}      # torch.dtype -> code
 _raw_stream = None  # device index -> handle of its current stream
 _int32_t = _float32_t = None
+_call = None      # lily_q4_call: one packed argument costs less than a score of them
+_ROPE = struct.Struct("18q").pack
+_ROWS = struct.Struct("13q").pack
+_ATTENTION = struct.Struct("5qd12q").pack
 
 
 def _first_use():
-    global _raw_stream, _int32_t, _float32_t
+    global _raw_stream, _int32_t, _float32_t, _call
     torch = _torch()
-    _raw_stream = torch._C._cuda_getCurrentRawStream
+    _call = load().lily_q4_call
     _int32_t, _float32_t = torch.int32, torch.float32
     _DTYPES.update({torch.bfloat16: BF16, torch.int16: BF16, torch.float16: F16, torch.float32: F32})
+    _raw_stream = torch._C._cuda_getCurrentRawStream
 
 
 def _dtype_code(t, what, f32=False):
@@ -474,36 +481,39 @@ class QKNormRope:
                                self.dtype or 0, int(bool(normalize)), float(eps),
                                float(weight_offset), float(rope_scale), _ptr(q_weight),
                                _ptr(k_weight), _ptr(turns) if rotary_dim else None)
-        self._ref = C.byref(self._c)
+        self._at = C.addressof(self._c)
 
     def c(self, dtype):
-        """The C struct by reference, for heads of this type."""
-        if self.dtype not in (None, dtype):
+        """The C struct's address, for heads of this type."""
+        if self.dtype is None:
+            self._c.dtype = dtype
+        elif self.dtype != dtype:
             raise Q4Error(ERR_INVALID_ARG, "lily_qk_norm_rope: weights and heads of two types")
-        self._c.dtype = dtype
-        return self._ref
+        return self._at
 
 
 def lily_qk_norm_rope(op: QKNormRope, q, k, pos, q_out, k_out, stream=None):
     """Norm and rotation of every head of q [T, q_heads, D] and k [T, k_heads, D] (views with any
     token and head strides) into q_out and k_out, which may be q and k; k may be None."""
-    T, hq, d = q.shape[0], q.shape[1], op.head_dim
+    T, hq, d = q.shape
     dtype = _dtype_code(q, "lily_qk_norm_rope")
-    if q_out.dtype != q.dtype or (k is not None and not k.dtype == k_out.dtype == q.dtype):
+    t = q.dtype
+    if q_out.dtype is not t or (k is not None and (k.dtype is not t or k_out.dtype is not t)):
         raise Q4Error(ERR_INVALID_ARG, "lily_qk_norm_rope: q, k and their outputs of one type")
-    hk, kr, ko = 0, (None, 0, 0), (None, 0, 0)
+    if d != op.head_dim:
+        raise Q4Error(ERR_INVALID_ARG, f"lily_qk_norm_rope: heads of {d}")
+    hk, kr, ko = 0, (0, 0, 0), (0, 0, 0)
     if k is not None:
         hk = k.shape[1]
         kr, ko = _rows(k, T, hk, d, "k"), _rows(k_out, T, hk, d, "k_out")
+    at = 0
     if op.rotary_dim:
-        _require(pos.numel() == T, "lily_qk_norm_rope: pos")
-        pos = _int32(pos, "pos")
-    else:
-        pos = None
-    rc = (_lib or load()).lily_qk_norm_rope(op.c(dtype), T, hq, hk, pos, *_rows(q, T, hq, d, "q"),
-                                            *_rows(q_out, T, hq, d, "q_out"), *kr, *ko,
-                                            _raw_stream(q.get_device()) if stream is None
-                                            else stream.cuda_stream)
+        at = _int32(pos, "pos")
+        if pos.numel() != T:
+            raise Q4Error(ERR_INVALID_ARG, "lily_qk_norm_rope: pos")
+    rc = _call(0, _ROPE(op.c(dtype), T, hq, hk, at, *_rows(q, T, hq, d, "q"),
+                        *_rows(q_out, T, hq, d, "q_out"), *kr, *ko,
+                        _raw_stream(q.get_device()) if stream is None else stream.cuda_stream))
     return rc if rc == OK else _check(rc, "lily_qk_norm_rope")
 
 
@@ -521,7 +531,7 @@ class KV8Cache:
         self.n_pages, self.kv_heads, self.page, self.head_dim = (int(n) for n in k.shape)
         self._c = lily_kv8_cache(_ptr(k), _ptr(v), _ptr(k_amax), _ptr(v_amax), self.n_pages,
                                  self.kv_heads, self.page, self.head_dim)
-        self._ref = C.byref(self._c)
+        self._at = C.addressof(self._c)
 
     @classmethod
     def new(cls, n_pages, kv_heads, page, head_dim, device="cuda"):
@@ -533,8 +543,8 @@ class KV8Cache:
         return cls(*codes, *amax)
 
     def c(self):
-        """The C struct by reference."""
-        return self._ref
+        """The C struct's address."""
+        return self._at
 
 
 class KV8Batch:
@@ -549,56 +559,58 @@ class KV8Batch:
         self._c = lily_kv8_batch(_int32(block_table, "block_table"), _int32(q_start, "q_start"),
                                  _int32(kv_len, "kv_len"), int(block_table.shape[1]), n, int(max_q),
                                  int(max_kv))
-        self._ref = C.byref(self._c)
+        self._at = C.addressof(self._c)
 
     def c(self):
-        """The C struct by reference."""
-        return self._ref
+        """The C struct's address."""
+        return self._at
 
 
-def _kv8_rows(fn, name, cache, batch, k, v, ws, stream, f32):
+def _kv8_rows(which, name, cache, batch, k, v, ws, stream, f32):
     T, h, d = k.shape[0], cache.kv_heads, cache.head_dim
     dtype = _dtype_code(k, name, f32)
-    if v.dtype != k.dtype:
+    if v.dtype is not k.dtype:
         raise Q4Error(ERR_INVALID_ARG, f"{name}: k and v of one type")
-    rc = fn(cache.c(), batch.c(), T, dtype, *_rows(k, T, h, d, "k"), *_rows(v, T, h, d, "v"),
-            *_space(ws), _raw_stream(k.get_device()) if stream is None else stream.cuda_stream)
+    rc = _call(which, _ROWS(cache._at, batch._at, T, dtype, *_rows(k, T, h, d, "k"),
+                            *_rows(v, T, h, d, "v"), *_space(ws),
+                            _raw_stream(k.get_device()) if stream is None else stream.cuda_stream))
     return rc if rc == OK else _check(rc, name)
 
 
 def _space(ws):
-    return (None, 0) if ws is None else (ws.data_ptr(), ws.numel() * ws.element_size())
+    return (0, 0) if ws is None else (ws.data_ptr(), ws.nbytes)
 
 
 def lily_kv8_append(cache: KV8Cache, batch: KV8Batch, k, v, ws=None, stream=None):
     """Writes the batch's tokens k, v [T, kv_heads, head_dim] into the cache; see include/lily_q4.h."""
-    return _kv8_rows((_lib or load()).lily_kv8_append, "lily_kv8_append", cache, batch, k, v, ws, stream, False)
+    return _kv8_rows(1, "lily_kv8_append", cache, batch, k, v, ws, stream, False)
 
 
 def lily_kv8_read(cache: KV8Cache, batch: KV8Batch, k_out, v_out, ws=None, stream=None):
     """The values of the batch's tokens into k_out, v_out (bf16, fp16 or fp32)."""
-    return _kv8_rows((_lib or load()).lily_kv8_read, "lily_kv8_read", cache, batch, k_out, v_out, ws, stream, True)
+    return _kv8_rows(2, "lily_kv8_read", cache, batch, k_out, v_out, ws, stream, True)
 
 
 def lily_kv8_attention_workspace_bytes(cache: KV8Cache, batch: KV8Batch, T: int, q_heads: int) -> int:
-    return int(load().lily_kv8_attention_workspace_bytes(cache.c(), batch.c(), int(T), int(q_heads)))
+    return int(load().lily_kv8_attention_workspace_bytes(C.byref(cache._c), C.byref(batch._c), int(T),
+                                                         int(q_heads)))
 
 
 def lily_kv8_attention(cache: KV8Cache, batch: KV8Batch, q, out, scale, lse=None, causal=True,
                        window=0, ws=None, stream=None):
     """Attention of q [T, q_heads, head_dim] over the batch's cached tokens into out (same shape)
     and, if given, lse fp32 [T, q_heads]; see include/lily_q4.h."""
-    T, heads, d = q.shape[0], q.shape[1], cache.head_dim
+    T, heads, d = q.shape
     dtype = _dtype_code(q, "lily_kv8_attention")
-    if out.dtype != q.dtype:
-        raise Q4Error(ERR_INVALID_ARG, "lily_kv8_attention: q and out of one type")
+    if out.dtype is not q.dtype or d != cache.head_dim:
+        raise Q4Error(ERR_INVALID_ARG, "lily_kv8_attention: q and out of one type, the cache's head_dim")
+    at = 0
     if lse is not None:
         if lse.shape != (T, heads) or lse.dtype is not _float32_t or not lse.is_contiguous():
             raise Q4Error(ERR_INVALID_ARG, "lily_kv8_attention: lse is fp32 [T, q_heads]")
-        lse = lse.data_ptr()
-    rc = (_lib or load()).lily_kv8_attention(cache.c(), batch.c(), T, heads, dtype, scale,
-                                             1 if causal else 0, window, *_rows(q, T, heads, d, "q"),
-                                             *_rows(out, T, heads, d, "out"), lse, *_space(ws),
-                                             _raw_stream(q.get_device()) if stream is None
-                                             else stream.cuda_stream)
+        at = lse.data_ptr()
+    rc = _call(3, _ATTENTION(cache._at, batch._at, T, heads, dtype, scale, 1 if causal else 0, window,
+                             *_rows(q, T, heads, d, "q"), *_rows(out, T, heads, d, "out"), at,
+                             *_space(ws),
+                             _raw_stream(q.get_device()) if stream is None else stream.cuda_stream))
     return rc if rc == OK else _check(rc, "lily_kv8_attention")

@@ -384,4 +384,34 @@ int lily_kv8_attention(const lily_kv8_cache *cache, const lily_kv8_batch *batch,
   return launch_kv8_attention(*cache, *batch, s, qr, orow, lse, ws, (cudaStream_t)stream);
 }
 
+int lily_q4_call(int32_t which, const void *words) {
+  if (!words || which < 0 || which > LILY_CALL_KV8_ATTENTION) return LILY_Q4_ERR_INVALID_ARG;
+  int64_t w[18];  // the words may be unaligned
+  memcpy(w, words, (which == LILY_CALL_KV8_APPEND || which == LILY_CALL_KV8_READ ? 13 : 18) * sizeof(int64_t));
+  auto ptr = [&](int i) { return reinterpret_cast<void *>(w[i]); };
+  auto i32 = [&](int i) { return (int32_t)w[i]; };
+  auto stream = [&](int i) { return reinterpret_cast<lily_q4_stream_t>(w[i]); };
+  const auto *cache = reinterpret_cast<const lily_kv8_cache *>(w[0]);
+  const auto *batch = reinterpret_cast<const lily_kv8_batch *>(w[1]);
+  switch (which) {
+    case LILY_CALL_QK_NORM_ROPE:
+      return lily_qk_norm_rope(reinterpret_cast<const lily_qk_rope *>(w[0]), i32(1), i32(2), i32(3),
+                               static_cast<const int32_t *>(ptr(4)), ptr(5), w[6], w[7], ptr(8), w[9], w[10],
+                               ptr(11), w[12], w[13], ptr(14), w[15], w[16], stream(17));
+    case LILY_CALL_KV8_APPEND:
+      return lily_kv8_append(cache, batch, i32(2), i32(3), ptr(4), w[5], w[6], ptr(7), w[8], w[9], ptr(10),
+                             (size_t)w[11], stream(12));
+    case LILY_CALL_KV8_READ:
+      return lily_kv8_read(cache, batch, i32(2), i32(3), ptr(4), w[5], w[6], ptr(7), w[8], w[9], ptr(10),
+                           (size_t)w[11], stream(12));
+    default: {
+      double scale;
+      memcpy(&scale, &w[5], sizeof(scale));
+      return lily_kv8_attention(cache, batch, i32(2), i32(3), i32(4), (float)scale, i32(6), i32(7), ptr(8), w[9],
+                                w[10], ptr(11), w[12], w[13], static_cast<float *>(ptr(14)), ptr(15), (size_t)w[16],
+                                stream(17));
+    }
+  }
+}
+
 }  // extern "C"

@@ -15,7 +15,12 @@
 //
 // Bound by memory: 2 bytes in and 1 byte out an element; at one token a sequence by the launch
 // and one chain of dependent reads (lengths, page number, magnitude).  A run is read once, held
-// in registers between finding its magnitude and writing its codes.
+// in registers between finding its magnitude and writing its codes.  Measured on one GB300: 11k
+// prompt tokens of 8 heads of 128 (keys and values, 69 MB): 22 us, 3.1 TB/s, half of the copy rate: a
+// block's chain of reads before its rows arrive, and about ten instructions an element (36 us with
+// one 256-thread block a run and a division an element).  16 sequences of one token: 3 us.
+//
+// Read, measured: 131,072 tokens of 2 heads of 256 to bf16 (403 MB): 65 us, 6.2 TB/s (91%).
 #include <algorithm>
 #include <type_traits>
 

@@ -1,26 +1,40 @@
 // lily_kv8_attention, the form for many rows a sequence (prompt chunks): tcgen05 tiles.
 //
-// Bound by the tensor cores (4 * head_dim operations a visible query-key pair).  A block takes 128
-// rows -- the group's heads of consecutive tokens of one key/value head, so that every code read
-// serves all of them -- and walks its visible keys 128 at a time:
+// Bound by the tensor cores (4 * head_dim operations a visible query-key pair).  A block takes row
+// tiles of 128 rows -- the group's heads of consecutive tokens of one key/value head, so that every
+// code read serves all of them -- and walks their visible keys 128 at a time:
 //   S = Q K^T (both in shared memory), P = 2^(S' - m) as fp16 written over S in tensor memory,
 //   O += P V (P from tensor memory, V from shared memory), O in tensor memory throughout.
-// Warps: 4 of softmax (a thread owns a row: its maximum and sum need no exchange), 4 (head_dim 256:
-// 8) that turn codes into fp16 operands, 1 that issues the products.
+// One block an SM, which holds all 512 TMEM columns.  Warps: 8 of softmax (a thread owns a row: its
+// maximum and sum need no exchange), 4 (head_dim 256: 8) that turn codes into fp16 operands, 1 that
+// issues the products.
 //
-// Operands.  K's codes keep their order; V's are transposed on the way (a lane holds 16 bytes of 8
-// consecutive tokens, byte permutes interleave the tokens), so both are K-major tiles with the
+// Head_dim 64 and 128: two row tiles a block share each converted key tile (S 2 x 128 columns, O 2 x
+// head_dim); K and V have two buffers.  While one tile's softmax runs, the other's products do.
+// Head_dim 256: one row tile (O 256 columns), S twice: the next key tile's scores are computed under
+// the softmax of the current one, and two softmax groups take the key tiles in turns, handing the
+// running maximum on.  K and V have one buffer (64 KB each); K's four atoms of 64 elements and V's two
+// halves of 64 keys are given back and refilled one by one.
+//
+// Operands.  K's codes keep their order; V's are transposed on the way (a lane holds 8 or 16 bytes of
+// 8 consecutive tokens, byte permutes interleave the tokens), so both are K-major tiles with the
 // 128-byte swizzle, written without bank conflicts.  Codes of the next tile are in flight in
-// registers while the current one is converted.  fp16 holds the codes exactly and q after a scaling
-// by a power of two; the weights are rounded to fp16 relative to the largest weight-times-magnitude
-// (see kv8_attention.cu for the magnitudes' place in the exponent).
-//
-// Layouts.  Head_dim 64 and 128: 256 TMEM columns a block (S 128, O 128) and two blocks an SM, whose
-// softmax and products fall into each other's gaps.  Head_dim 256: one block an SM, O takes 256
-// columns and S is held twice, so the next S is computed under the softmax of the current one.
+// registers meanwhile; nothing is computed from a load before it is needed (a select after a load
+// waits for it: 1449 -> 800 us came mostly from removing such waits).  fp16 holds the codes exactly and
+// q after a scaling by a power of two; the weights are rounded to fp16 relative to the largest
+// weight-times-magnitude (see kv8_attention.cu for the magnitudes' place in the exponent).
 //
 // The running maximum moves only when a row's grows by more than 2^8 (weights up to 256 are as exact
 // in fp16), because moving it rescales O in tensor memory.
+//
+// Measured on one GB300: 5 ragged prompts, 6.6k tokens over up to 8k keys each, 32 / 8 heads of 128: 667 us
+// (955 TFLOP/s, 50% of the measured bf16 rate); a 4096-token chunk after 28,672, 16 / 2 heads of 256:
+// 2.11 ms (976 TFLOP/s, 51%).  What bounds it: at 128, the chain of one row tile (scores 540 cycles,
+// maximum 570, weights 1,750, product 870, hand-overs 700) against the other's, with the SM issuing
+// 44% of the time; at 256 conversion and products about equally (without conversion 1.61 ms, with a
+// quarter of the products 1.82 ms).  Tried without gain: four softmax groups of half a row each
+// (751 us), issuing whichever row tile is ready (886 us), starting the product after half of the
+// weights, longer suspension in barrier waits.
 #include <algorithm>
 
 #include "kv8_device.cuh"

@@ -16,6 +16,10 @@
 // 64-bit integers is the angle of any 32-bit position without loss; its top 32 bits, taken as
 // signed, are the angle in [-1/2, 1/2) turns, which sincospif takes after a rounding of
 // 2^-24 relative.  A 32-bit float product would be off by 0.06 rad at position 10^6.
+//
+// Measured on one GB300: 8192 tokens, 40 heads of 128 (168 MB): 35 us, 4.8 TB/s, 70% of the copy rate
+// (52 us with a block a token and its angles behind a block barrier; the rest is instruction issue, about
+// 130 a head and lane); one token of 18 heads of 256: 2.4 us.
 #include <algorithm>
 #include <cmath>
 

@@ -424,6 +424,18 @@ LILY_Q4_API size_t lily_kv8_attention_workspace_bytes(const lily_kv8_cache *cach
                                                       const lily_kv8_batch *batch, int32_t T,
                                                       int32_t q_heads);
 
+/*
+ * lily_q4_call -- one of the attention calls with its arguments in an array of 64-bit words, in the
+ * order of its own declaration (integers sign-extended, pointers as integers, `scale` as the bits
+ * of a double), for foreign-function interfaces whose cost an argument shows in single-token
+ * steps.  The typed calls above are the interface; this one only forwards to them.
+ */
+#define LILY_CALL_QK_NORM_ROPE 0 /* 18 words */
+#define LILY_CALL_KV8_APPEND 1   /* 13 words */
+#define LILY_CALL_KV8_READ 2     /* 13 words */
+#define LILY_CALL_KV8_ATTENTION 3 /* 18 words */
+LILY_Q4_API int lily_q4_call(int32_t which, const void *words);
+
 /* Human-readable name of a status code (static string). */
 LILY_Q4_API const char *lily_q4_status_string(int status);
 

@@ -169,3 +169,83 @@ def test_attention_workspace(lib):
 
 def test_status_of_bad_indices(lib):
     assert "out of range" in q4.status_string(q4.ERR_INDEX)
+
+
+# --------------------------------------------------------------------------- the packed call
+
+def test_packed_call_forwards(lib):
+    """The same statuses as the typed calls, from the words in their order."""
+    import struct
+    op, cache, batch = _op(), _cache(), _batch()
+    rows = [FAKE, 1024, 128]
+    rope = lambda T, q: struct.pack("18q", C.addressof(op), T, 4, 2, FAKE, q, 1024, 128, *rows, *rows, *rows, 0)
+    assert lib.lily_q4_call(0, rope(0, 0)) == q4.OK
+    assert lib.lily_q4_call(0, rope(2, 0)) == q4.ERR_INVALID_ARG
+    for which in (1, 2):
+        words = lambda T, dt, n: struct.pack("13q", C.addressof(cache), C.addressof(batch), T, dt, *rows, *rows, FAKE, n, 0)
+        assert lib.lily_q4_call(which, words(0, 0, 256)) == q4.OK
+        assert lib.lily_q4_call(which, words(6, 3, 256)) == q4.ERR_UNSUPPORTED
+        assert lib.lily_q4_call(which, words(6, 0, 255)) == q4.ERR_WORKSPACE_TOO_SMALL
+    att = lambda T, scale, n: struct.pack("5qd12q", C.addressof(cache), C.addressof(batch), T, 8, 0, scale, 1, 0,
+                                          *rows, *rows, 0, FAKE, n, 0)
+    assert lib.lily_q4_call(3, att(0, 0.1, 0)) == q4.OK
+    assert lib.lily_q4_call(3, att(6, float("nan"), 1 << 30)) == q4.ERR_INVALID_ARG
+    assert lib.lily_q4_call(3, att(6, 0.1, 256)) == q4.ERR_WORKSPACE_TOO_SMALL
+    assert lib.lily_q4_call(4, att(0, 0.1, 0)) == q4.ERR_INVALID_ARG
+    assert lib.lily_q4_call(0, None) == q4.ERR_INVALID_ARG
+
+
+class _Stream:
+    cuda_stream = 0
+
+
+def _tensors():
+    import torch
+    cache = q4.KV8Cache.new(3, 2, 16, 64, device="cpu")
+    i32 = lambda *a: torch.tensor(a, dtype=torch.int32)
+    batch = q4.KV8Batch(i32(0, 1).reshape(1, 2), i32(0, 1), i32(1), 1, 20)
+    return torch, cache, batch
+
+
+@pytest.mark.parametrize("bad", ["heads", "dim", "dtype", "mixed", "dense", "lse", "no workspace"])
+def test_binding_refuses_attention(lib, bad):
+    torch, cache, batch = _tensors()
+    q = torch.zeros((1, 4, 64), dtype=torch.bfloat16)
+    out, lse, ws = q.clone(), torch.zeros((1, 4)), torch.zeros(1 << 20, dtype=torch.uint8)
+    if bad == "heads":
+        out = out[:, :3]
+    elif bad == "dim":
+        q, out = (torch.zeros((1, 4, 128), dtype=torch.bfloat16) for _ in "qo")
+    elif bad == "dtype":
+        q, out = q.float(), out.float()
+    elif bad == "mixed":
+        out = out.half()
+    elif bad == "dense":
+        q = torch.zeros((1, 64, 4), dtype=torch.bfloat16).transpose(1, 2)
+    elif bad == "lse":
+        lse = lse.double()
+    else:
+        ws = None
+    with pytest.raises(q4.Q4Error):
+        q4.lily_kv8_attention(cache, batch, q, out, 0.1, lse=lse, ws=ws, stream=_Stream)
+
+
+def test_binding_refuses_the_rest(lib):
+    torch, cache, batch = _tensors()
+    ws = torch.zeros(256, dtype=torch.uint8)
+    k = torch.zeros((1, 2, 64), dtype=torch.bfloat16)
+    for a, b in ((k[:, :1], k), (k, k.half()), (k.float(), k.float()), (k[..., :32], k[..., :32])):
+        with pytest.raises(q4.Q4Error):
+            q4.lily_kv8_append(cache, batch, a, b, ws=ws, stream=_Stream)
+    op = q4.QKNormRope(64, 64, torch.zeros(32, dtype=torch.int64))
+    pos = torch.zeros(1, dtype=torch.int32)
+    for q, o, p in ((k, k, pos.long()), (k, k.half(), pos), (k, k[:, :1], pos), (k[..., :32], k[..., :32], pos),
+                    (k, k, torch.zeros(2, dtype=torch.int32))):
+        with pytest.raises(q4.Q4Error):
+            q4.lily_qk_norm_rope(op, q, None, p, o, None, stream=_Stream)
+    with pytest.raises(q4.Q4Error):
+        q4.QKNormRope(64, 64, torch.zeros(31, dtype=torch.int64))
+    with pytest.raises(q4.Q4Error):
+        q4.KV8Cache(cache.k, cache.v, cache.k_amax[:2], cache.v_amax)
+    with pytest.raises(q4.Q4Error):
+        q4.KV8Batch(torch.zeros((1, 2), dtype=torch.int64), pos, pos, 1, 1)
