@@ -226,12 +226,13 @@ __global__ void __launch_bounds__(PromptShape<D>::THREADS, 1)
     tc::mbar_init(drain, 1);
     tc::mbar_init_fence();
   }
+  if (tid < kRows) s_max[tid] = -INFINITY;
+  pdl_wait();
+  // after the wait: no tensor memory is held while a kernel that may want some is waited for
   if (warp == 0) {
     tc::tmem_alloc(tc::smem_u32(&s_tmem), 512);
     tc::tmem_relinquish();
   }
-  if (tid < kRows) s_max[tid] = -INFINITY;
-  pdl_wait();
   const Batch &B = a.B;
   int32_t *err = a.hdr + kHdrError;
   volatile int *abort_flag = &s_abort;
