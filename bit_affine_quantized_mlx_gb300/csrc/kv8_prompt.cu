@@ -148,27 +148,6 @@ constexpr uint32_t idesc_f16(int N) {  // D fp32, A and B fp16, both K-major, 12
   return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(kRows >> 4) << 24);
 }
 
-// Two fp32 lanes of one instruction: half the issue slots of the softmax's products and sums.
-__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-__device__ __forceinline__ float2 unpack2(uint64_t v) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-  return r;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
@@ -612,13 +591,12 @@ __global__ void __launch_bounds__(PromptShape<D>::THREADS, 1)
       for (int k = 0; k < P::VW; ++k) {
         uint32_t z[4][2];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t x = vr[2 * i][k] ^ 0x80808080u, y = vr[2 * i + 1][k] ^ 0x80808080u;
-          z[i][0] = __byte_perm(x, y, pair0);
-          z[i][1] = __byte_perm(x, y, pair1);
-        }
-#pragma unroll
         for (int e = 0; e < 4; ++e) {
+          if (e % 2 == 0) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              z[i][e >> 1] = __byte_perm(vr[2 * i][k], vr[2 * i + 1][k], e ? pair1 : pair0) ^ 0x80808080u;
+          }
           const uint32_t pick = e & 1 ? kPickHi : kPickLo;
           *reinterpret_cast<uint4 *>(atom + tc::sw128(d0 + 4 * k + (e ^ dg), tg)) =
               make_uint4(codes_f16(z[0][e >> 1], pick), codes_f16(z[1][e >> 1], pick),
@@ -666,12 +644,12 @@ __global__ void __launch_bounds__(PromptShape<D>::THREADS, 1)
         page = next;
       }
     } else if (warp < 12) {
-      // one buffer of K, whose four atoms come free and are filled one after the other; two atoms'
-      // codes are under way
-      uint4 kr[2][4];
+      // one buffer of K, whose four atoms come free and are filled one after the other; the next
+      // tile's codes are under way
+      uint4 kr[ATOMS][4];
       find_k(0, page0);
-      load_k(kr[0], 0);
-      load_k(kr[1], 1);
+#pragma unroll
+      for (int i = 0; i < ATOMS; ++i) load_k(kr[i], i);
       bool ok = true;
       for (int j = 0; j < tiles && ok; ++j) {
         const int next = page_of(j + 2, lane & 7);
@@ -679,10 +657,10 @@ __global__ void __launch_bounds__(PromptShape<D>::THREADS, 1)
         for (int i = 0; i < ATOMS; ++i) {
           ok = ok && free_wait(k_free + 8 * i, j);
           if (!ok) break;
-          store_k(kr[i & 1], mem + kAt + i * (kKeys * 128));
+          store_k(kr[i], mem + kAt + i * (kKeys * 128));
           publish(k_full + 8 * i);
-          if (i == ATOMS - 2) find_k(j + 1, page);
-          load_k(kr[i & 1], (i + 2) % ATOMS);
+          if (i == 0) find_k(j + 1, page);
+          load_k(kr[i], i);
         }
         page = next;
       }

@@ -17,9 +17,9 @@
 // signed, are the angle in [-1/2, 1/2) turns, which sincospif takes after a rounding of
 // 2^-24 relative.  A 32-bit float product would be off by 0.06 rad at position 10^6.
 //
-// Measured on one GB300: 8192 tokens, 40 heads of 128 (168 MB): 35 us, 4.8 TB/s, 70% of the copy rate
-// (52 us with a block a token and its angles behind a block barrier; the rest is instruction issue, about
-// 130 a head and lane); one token of 18 heads of 256: 2.4 us.
+// Measured on one GB300: 8192 tokens, 40 heads of 128 (168 MB): 30 us, 5.6 TB/s, 82% of the copy rate (52 us
+// with a block a token and its angles behind a block barrier, 35 with single instead of paired fp32
+// instructions: the rest is instruction issue); one token of 18 heads of 256: 2.4 us.
 #include <algorithm>
 #include <cmath>
 
@@ -46,7 +46,7 @@ enum RopePairs { kPairsNear, kPairsHalf, kPairsHalfOdd };
 
 // LANES a head; kRopeAhead passes (32 / LANES heads each) are loaded together.
 template <typename Ty, int PAIRS, int LANES>
-__global__ void __launch_bounds__(32 * kRopeWarps, PAIRS == kPairsHalfOdd ? 6 : 9)
+__global__ void __launch_bounds__(32 * kRopeWarps, PAIRS == kPairsHalfOdd ? 6 : 7)
     qk_norm_rope_kernel(RopeArgs a, int shares) {
   constexpr int GROUPS = 32 / LANES;
   __shared__ __align__(16) float2 s_cs[kRopeWarps][128];
@@ -66,7 +66,7 @@ __global__ void __launch_bounds__(32 * kRopeWarps, PAIRS == kPairsHalfOdd ? 6 : 
   const int heads = a.part[0].heads + a.part[1].heads, per = (heads + shares - 1) / shares;
   const int from = share * per, to = min(heads, from + per);
   float2 *cs_of = s_cs[warp];
-  float2 cs[4];
+  uint64_t co[2], si[2], no[2];  // cosines, sines and their negatives of the lane's four pairs
   bool angles = false;
   const float inv_d = 1.f / (float)a.D;
 
@@ -101,21 +101,35 @@ __global__ void __launch_bounds__(32 * kRopeWarps, PAIRS == kPairsHalfOdd ? 6 : 
 #pragma unroll
       for (int j = 0; j < 8; ++j) wt[j] += a.offset;
     }
+    // the lane's elements as first and second members of its pairs, two pairs together
+    uint64_t w2[2][2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      w2[0][j] = PAIRS == kPairsNear ? pack2(wt[4 * j], wt[4 * j + 2]) : pack2(wt[2 * j], wt[2 * j + 1]);
+      w2[1][j] = PAIRS == kPairsNear ? pack2(wt[4 * j + 1], wt[4 * j + 3]) : pack2(wt[4 + 2 * j], wt[5 + 2 * j]);
+    }
     if (!angles) {  // the loads are under way
       angles = true;
       if (half > 0) {
         const uint64_t pos = (uint64_t)(int64_t)a.pos[t];
         for (int i = lane; i < half; i += 32) {
-          float sn, co;
-          sincospif((float)(int32_t)((pos * a.turns[i]) >> 32) * 0x1p-31f, &sn, &co);
-          cs_of[i] = make_float2(co * a.rope_scale, sn * a.rope_scale);
+          float sn, cn;
+          sincospif((float)(int32_t)((pos * a.turns[i]) >> 32) * 0x1p-31f, &sn, &cn);
+          cs_of[i] = make_float2(cn * a.rope_scale, sn * a.rope_scale);
         }
         __syncwarp();
       }
       // pairs beyond R turn by nothing
+      float2 cs[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j)
         cs[j] = PAIRS != kPairsHalfOdd && live && 4 * c + j < half ? cs_of[4 * c + j] : make_float2(1.f, 0.f);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        co[j] = pack2(cs[2 * j].x, cs[2 * j + 1].x);
+        si[j] = pack2(cs[2 * j].y, cs[2 * j + 1].y);
+        no[j] = pack2(-cs[2 * j].y, -cs[2 * j + 1].y);
+      }
     }
     for (int base = h_begin; base < h_end; base += kRopeAhead * GROUPS) {
       if (base > h_begin) load();
@@ -124,15 +138,45 @@ __global__ void __launch_bounds__(32 * kRopeWarps, PAIRS == kPairsHalfOdd ? 6 : 
         if (base + i * GROUPS >= h_end) break;  // the same for every lane
         float y[8];
         unpack8<Ty>(make_uint4(raw[i][0].x, raw[i][0].y, raw[i][1].x, raw[i][1].y), y);
-        if (a.normalize) {
-          float ss = 0.f;
+        uint64_t u[2], v[2];
 #pragma unroll
-          for (int j = 0; j < 8; ++j) ss = fmaf(y[j], y[j], ss);
+        for (int j = 0; j < 2; ++j) {
+          u[j] = PAIRS == kPairsNear ? pack2(y[4 * j], y[4 * j + 2]) : pack2(y[2 * j], y[2 * j + 1]);
+          v[j] = PAIRS == kPairsNear ? pack2(y[4 * j + 1], y[4 * j + 3]) : pack2(y[4 + 2 * j], y[5 + 2 * j]);
+        }
+        if (a.normalize) {
+          uint64_t s2 = mul2(u[0], u[0]);
+          s2 = fma2(u[1], u[1], s2);
+          s2 = fma2(v[0], v[0], s2);
+          s2 = fma2(v[1], v[1], s2);
+          const float2 both = unpack2(s2);
+          float ss = both.x + both.y;
 #pragma unroll
           for (int o = LANES / 2; o; o >>= 1) ss += __shfl_xor_sync(~0u, ss, o);
           const float rs = rsqrtf(fmaf(ss, inv_d, a.eps));
+          const uint64_t rs2 = pack2(rs, rs);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) y[j] *= rs * wt[j];
+          for (int j = 0; j < 2; ++j) {
+            u[j] = mul2(u[j], mul2(rs2, w2[0][j]));
+            v[j] = mul2(v[j], mul2(rs2, w2[1][j]));
+          }
+        }
+        if (PAIRS != kPairsHalfOdd) {
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const uint64_t x = fma2(u[j], co[j], mul2(v[j], no[j]));
+            v[j] = fma2(u[j], si[j], mul2(v[j], co[j]));
+            u[j] = x;
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const float2 p = unpack2(u[j]), q = unpack2(v[j]);
+          if (PAIRS == kPairsNear) {
+            y[4 * j] = p.x, y[4 * j + 2] = p.y, y[4 * j + 1] = q.x, y[4 * j + 3] = q.y;
+          } else {
+            y[2 * j] = p.x, y[2 * j + 1] = p.y, y[4 + 2 * j] = q.x, y[5 + 2 * j] = q.y;
+          }
         }
         if (PAIRS == kPairsHalfOdd) {
           float *row = s_row + warp * 256 + (lane - c) * 8;
@@ -150,15 +194,6 @@ __global__ void __launch_bounds__(32 * kRopeWarps, PAIRS == kPairsHalfOdd ? 6 : 
               y[j] = low ? y[j] * k.x - other * k.y : other * k.y + y[j] * k.x;
             }
           }
-        } else {
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            float &u = PAIRS == kPairsNear ? y[2 * j] : y[j];
-            float &v = PAIRS == kPairsNear ? y[2 * j + 1] : y[4 + j];
-            const float x = u * cs[j].x - v * cs[j].y;
-            v = u * cs[j].y + v * cs[j].x;
-            u = x;
-          }
         }
         if (left > i * GROUPS) {
           const uint4 o = pack8<Ty>(y);
@@ -175,11 +210,12 @@ __global__ void __launch_bounds__(32 * kRopeWarps, PAIRS == kPairsHalfOdd ? 6 : 
 
 template <typename Ty, int PAIRS, int LANES>
 static cudaError_t launch_lanes(const RopeArgs &a, cudaStream_t st) {
-  // A token's heads are shared out until there are about three warps for each that fits on the GPU,
-  // down to one pass a warp, at the price of computing the token's sines in each.
+  // A token's heads are shared out until there are about two warps for each that fits on the GPU (28 an
+  // SM), down to one pass a warp, at the price of computing the token's sines in each (8192 tokens of
+  // 40 heads of 128: 30 us with a warp a token, 32 with two, 37 with four).
   const int passes = (a.part[0].heads + a.part[1].heads + 32 / LANES - 1) / (32 / LANES);
   const int sms = sm_count() > 0 ? sm_count() : 1;
-  const int shares = std::max(1, std::min(passes, 3 * 36 * sms / a.T));
+  const int shares = std::max(1, std::min(passes, 54 * sms / a.T));
   const int64_t tasks = (int64_t)a.T * shares;
   return launch_pdl(qk_norm_rope_kernel<Ty, PAIRS, LANES>, dim3((unsigned)((tasks + kRopeWarps - 1) / kRopeWarps)),
                     dim3(32 * kRopeWarps), 0, st, a, shares);
