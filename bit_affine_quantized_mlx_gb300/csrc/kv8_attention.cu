@@ -110,7 +110,9 @@ __global__ void __launch_bounds__(kDecThreads, decode_blocks(D, NT)) kv8_decode_
   constexpr int RING = ring_bytes(D, NT);
   extern __shared__ __align__(128) uint8_t smem[];
   uint8_t *s_q = smem + kDecWarps * RING;
-  float *s_meta = reinterpret_cast<float *>(s_q + RT * QS);  // [warp][stage][2][NG]
+  float2 *s_fin = reinterpret_cast<float2 *>(s_q + RT * QS);     // [RT]: maximum and sum of the segment
+  int2 *s_row = reinterpret_cast<int2 *>(s_fin + RT);            // [RT]: row (or -1) and query head
+  float *s_meta = reinterpret_cast<float *>(s_row + RT);         // [warp][stage][2][NG]
   float *s_qf = s_meta + kDecWarps * kDecStages * 2 * NG;    // [RT]
   float *s_m = s_qf + RT, *s_l = s_m + kDecWarps * RT;       // [warp][RT]
   int *s_scan = reinterpret_cast<int *>(s_l + kDecWarps * RT);  // [4]
@@ -182,7 +184,20 @@ __global__ void __launch_bounds__(kDecThreads, decode_blocks(D, NT)) kv8_decode_
     const int t1 = min(ntile, t0 + end - cur);
     const int h = item % a.kv_heads, rt = item / a.kv_heads;
 
-    // ---- this warp's turns, the first of them under way before q is read: turn i holds tokens first + i * TILE ...
+    // ---- q's words under way (a warp takes rows warp, warp + 4 ...) before the pages are looked up
+    constexpr int E = D / 32, QR = RT / kDecWarps;
+    uint32_t qw[QR][E / 2];
+#pragma unroll
+    for (int k = 0; k < QR; ++k) {
+      const RowOf ro = row_of(sq, rt * RT + warp + k * kDecWarps, h, a.group);
+      const uint32_t *src = reinterpret_cast<const uint32_t *>(
+          a.q + (int64_t)ro.row * a.q_ts + (int64_t)ro.head * a.q_hs + lane * E);
+#pragma unroll
+      for (int i = 0; i < E / 2; ++i) qw[k][i] = ro.row >= 0 ? __ldg(src + i) : 0;
+      if (lane == 0) s_row[warp + k * kDecWarps] = make_int2(ro.row, ro.head);
+    }
+
+    // ---- this warp's turns, the first of them under way before q is converted: turn i holds tokens first + i * TILE ...
     const int first = lo + (t0 * kDecWarps + warp) * WS;
     const int turns = min(t1 - t0, max(0, (hi - first + TILE - 1) / TILE));
     auto page_of = [&](int idx) {  // page of 16-token group idx of this warp's turns
@@ -230,19 +245,14 @@ __global__ void __launch_bounds__(kDecThreads, decode_blocks(D, NT)) kv8_decode_
       tc::cp_async_commit();
     }
     // ---- q, scaled by a power of two for each row so that its largest element is in [2^14, 2^15)
-    for (int r = warp; r < RT; r += kDecWarps) {
-      constexpr int E = D / 32;
-      const RowOf ro = row_of(sq, rt * RT + r, h, a.group);
+#pragma unroll
+    for (int k = 0; k < QR; ++k) {
+      const int r = warp + k * kDecWarps;
       float f[E];
       float top = 0.f;
-      const uint16_t *src = a.q + (int64_t)ro.row * a.q_ts + (int64_t)ro.head * a.q_hs + lane * E;
 #pragma unroll
       for (int i = 0; i < E / 2; ++i) {
-        float2 p = make_float2(0.f, 0.f);
-        if (ro.row >= 0) {
-          const uint32_t w = reinterpret_cast<const uint32_t *>(src)[i];
-          p = bf16 ? Bf16::to_f32x2(w) : F16::to_f32x2(w);
-        }
+        const float2 p = bf16 ? Bf16::to_f32x2(qw[k][i]) : F16::to_f32x2(qw[k][i]);
         f[2 * i] = p.x;
         f[2 * i + 1] = p.y;
         top = fmaxf(top, fmaxf(fabsf(p.x), fabsf(p.y)));
@@ -455,6 +465,18 @@ __global__ void __launch_bounds__(kDecThreads, decode_blocks(D, NT)) kv8_decode_
         }
       }
     __syncthreads();
+    if (tid < RT) {
+      float top = s_m[tid], den = 0.f;
+#pragma unroll
+      for (int w = 1; w < kDecWarps; ++w) top = fmaxf(top, s_m[w * RT + tid]);
+#pragma unroll
+      for (int w = 0; w < kDecWarps; ++w) {
+        const float mw = s_m[w * RT + tid];
+        // without a maximum the sum is 0, or NaN for a row of NaN
+        den += s_l[w * RT + tid] * (mw == -INFINITY ? 1.f : ex2(mw - top));
+      }
+      s_fin[tid] = make_float2(top, den);
+    }
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -475,34 +497,27 @@ __global__ void __launch_bounds__(kDecThreads, decode_blocks(D, NT)) kv8_decode_
     const int slot = 2 * blockIdx.x + (cur == begin ? 0 : 1);
     for (int e = tid; e < RT * (D / 2); e += kDecThreads) {
       const int r = e / (D / 2), d = (e - r * (D / 2)) * 2;
-      const RowOf ro = row_of(sq, rt * RT + r, h, a.group);
-      if (ro.row < 0) continue;
+      const int2 ro = s_row[r];
+      if (ro.x < 0) continue;
+      const float2 fin = s_fin[r];
       float2 sum = make_float2(0.f, 0.f);
-      float top = s_m[r], den = 0.f;
 #pragma unroll
       for (int w = 0; w < kDecWarps; ++w) {
         const float2 u = *reinterpret_cast<const float2 *>(
             reinterpret_cast<const float *>(smem + w * RING) + r * OS + d);
         sum.x += u.x;
         sum.y += u.y;
-        top = fmaxf(top, s_m[w * RT + r]);
-      }
-#pragma unroll
-      for (int w = 0; w < kDecWarps; ++w) {
-        const float mw = s_m[w * RT + r];
-        // without a maximum the sum is 0, or NaN for a row of NaN
-        den += s_l[w * RT + r] * (mw == -INFINITY ? 1.f : ex2(mw - top));
       }
       if (split) {
         *reinterpret_cast<float2 *>(a.part + ((int64_t)slot * RT + r) * D + d) = sum;
-        if (d == 0) a.ml[slot * RT + r] = make_float2(top, den);
+        if (d == 0) a.ml[slot * RT + r] = fin;
       } else {
-        const float f = den == 0.f ? 0.f : 1.f / (127.f * den);
+        const float f = fin.y == 0.f ? 0.f : 1.f / (127.f * fin.y);
         const uint32_t w = bf16 ? Bf16::from_f32x2(sum.x * f, sum.y * f) : F16::from_f32x2(sum.x * f, sum.y * f);
-        *reinterpret_cast<uint32_t *>(a.out + (int64_t)ro.row * a.o_ts + (int64_t)ro.head * a.o_hs + d) = w;
+        *reinterpret_cast<uint32_t *>(a.out + (int64_t)ro.x * a.o_ts + (int64_t)ro.y * a.o_hs + d) = w;
         if (d == 0 && a.lse)
-          a.lse[(int64_t)ro.row * a.kv_heads * a.group + ro.head] =
-              den == 0.f ? -INFINITY : (top + log2f(den)) * 0.69314718056f;
+          a.lse[(int64_t)ro.x * a.kv_heads * a.group + ro.y] =
+              fin.y == 0.f ? -INFINITY : (fin.x + log2f(fin.y)) * 0.69314718056f;
       }
     }
     if (split && t0 == 0 && tid == 0) {
@@ -655,7 +670,7 @@ static DecodePlan decode_plan(const lily_kv8_cache &C, const lily_kv8_batch &b, 
   p.items = (int)std::min<int64_t>(items, p.grid);
   p.rows = (int)std::min<int64_t>(RT, rows);
   const int ng = kTurnBytes / D / 16;
-  p.smem = kDecWarps * ring_bytes(D, p.nt) + RT * (D * 2 + 16) +
+  p.smem = kDecWarps * ring_bytes(D, p.nt) + RT * (D * 2 + 16 + 16) +
            4 * (kDecWarps * kDecStages * 2 * ng + RT + 2 * kDecWarps * RT + 4 + b.batch + 1);
   size_t off = kAlign;
   p.off_jobs = off;
