@@ -7,8 +7,8 @@
 // tiles of 8 * NT rows.
 //
 // Split.  The work is a list of (sequence, row tile, key/value head) items, each a row of tiles of
-// keys; the tiles of all items, laid end to end, are cut into equal shares, one a block, whatever
-// the lengths are.  An item that lies within one share is finished by its block; the parts of one
+// keys; the tiles of all items (and what it costs to begin one, in tiles), laid end to end, are cut into
+// equal shares, one a block, whatever the lengths are.  An item that lies within one share is finished by its block; the parts of one
 // that crosses shares go to the workspace (running maximum, sum, unnormalised output) and a second
 // launch joins them in the order of the keys.  Lengths are read on the device, so a captured graph
 // follows them.
@@ -46,6 +46,10 @@
 namespace lq4 {
 
 constexpr int kDecThreads = 128, kDecWarps = 4, kDecStages = 2;
+// What beginning an item costs a block (its lengths, pages, queries and the join of its warps), in tiles:
+// items are that much longer when they are shared out, so that a block with the ends of two has
+// fewer tiles (16 x 3 tokens over 4096 keys, 96 items of 17 tiles: 18.5 us without).
+constexpr int kStart = 2;
 constexpr int kTurnBytes = 4096;  // of keys, and of values, a warp and turn
 
 __device__ __forceinline__ float ex2(float x) {
@@ -135,7 +139,7 @@ __global__ void __launch_bounds__(kDecThreads, decode_blocks(D, NT)) kv8_decode_
       if (s.n > 0) {
         int lo, nt;
         range_of(s, lo, nt);
-        count = (s.n * a.group + RT - 1) / RT * a.kv_heads * nt;
+        count = (s.n * a.group + RT - 1) / RT * a.kv_heads * (nt + kStart);
       }
     }
     int sum = count;
@@ -156,7 +160,7 @@ __global__ void __launch_bounds__(kDecThreads, decode_blocks(D, NT)) kv8_decode_
     a.jobs[2 * blockIdx.x] = make_int4(-1, 0, 0, 0);
   }
   __syncthreads();
-  // equal shares of the tiles; with fewer tiles than blocks the last blocks have none
+  // equal shares of the work; with less of it than blocks the last blocks have none
   const int64_t total = s_pre[B.batch], G = min((int64_t)gridDim.x, total);
   if (blockIdx.x >= G) return;
   const int begin = (int)(total * blockIdx.x / G), end = (int)(total * (blockIdx.x + 1) / G);
@@ -180,8 +184,12 @@ __global__ void __launch_bounds__(kDecThreads, decode_blocks(D, NT)) kv8_decode_
     int lo, ntile;
     range_of(sq, lo, ntile);
     const int hi = sq.len;
-    const int local = cur - s_pre[b], item = local / ntile, t0 = local - item * ntile;
-    const int t1 = min(ntile, t0 + end - cur);
+    const int per = ntile + kStart, local = cur - s_pre[b], item = local / per, u0 = local - item * per;
+    const int u1 = min(per, u0 + end - cur), t0 = max(u0 - kStart, 0), t1 = max(u1 - kStart, 0);
+    if (t0 >= t1) {  // a share that ends before the item's first tile
+      cur += u1 - u0;
+      continue;
+    }
     const int h = item % a.kv_heads, rt = item / a.kv_heads;
 
     // ---- q's words under way (a warp takes rows warp, warp + 4 ...) before the pages are looked up
@@ -522,13 +530,13 @@ __global__ void __launch_bounds__(kDecThreads, decode_blocks(D, NT)) kv8_decode_
     }
     if (split && t0 == 0 && tid == 0) {
       // the block that holds the item's last tile: the largest c with floor(c total / G) <= it
-      const int64_t last = cur + ntile - 1;
+      const int64_t last = cur - u0 + per - 1;
       const int c_last = (int)(((last + 1) * G - 1) / total);
       a.jobs[2 * blockIdx.x] = make_int4(sq.row0, sq.n, h, rt);
       a.jobs[2 * blockIdx.x + 1] = make_int4(slot, c_last, 0, 0);
     }
     __syncthreads();
-    cur += t1 - t0;
+    cur += u1 - u0;
   }
 }
 
@@ -661,8 +669,8 @@ static DecodePlan decode_plan(const lily_kv8_cache &C, const lily_kv8_batch &b, 
   const int sms = sm_count() > 0 ? sm_count() : 152;
   const int64_t items = std::min<int64_t>(b.batch, T) * ((rows + RT - 1) / RT) * C.kv_heads;
   const int64_t tiles = std::max<int64_t>(1, ((int64_t)b.max_kv + 16 + tile - 1) / tile);
-  if (items > INT32_MAX / tiles) return p;  // total 0: the tiles have to be countable in 31 bits
-  p.grid = (int)std::max<int64_t>(1, std::min<int64_t>(std::min(decode_blocks(D, p.nt) * sms, kJoinMost), items * tiles));
+  if (items > INT32_MAX / (tiles + kStart)) return p;  // total 0: the tiles have to be countable in 31 bits
+  p.grid = (int)std::max<int64_t>(1, std::min<int64_t>(std::min(decode_blocks(D, p.nt) * sms, kJoinMost), items * (tiles + kStart)));
   // Few items have many parts each: a large block reads a row's parts together (262,144 tokens, 152
   // parts: 12 us with 256 threads, 8 with 512).  Fewer: small blocks start
   // faster (64 sequences, 512 items: 6 us with 256 threads, 10 with 512).
