@@ -27,9 +27,9 @@
 // The running maximum moves only when a row's grows by more than 2^8 (weights up to 256 are as exact
 // in fp16), because moving it rescales O in tensor memory.
 //
-// Measured on one GB300: 5 ragged prompts, 6.6k tokens over up to 8k keys each, 32 / 8 heads of 128: 667 us
-// (955 TFLOP/s, 50% of the measured bf16 rate); a 4096-token chunk after 28,672, 16 / 2 heads of 256:
-// 2.11 ms (976 TFLOP/s, 51%).  What bounds it: at 128, the chain of one row tile (scores 540 cycles,
+// Measured on one GB300: 5 ragged prompts, 6.6k tokens over up to 8k keys each, 32 / 8 heads of 128: 649 us
+// (981 TFLOP/s, 51% of the measured bf16 rate); a 4096-token chunk after 28,672, 16 / 2 heads of 256:
+// 2.08 ms (990 TFLOP/s, 52%).  What bounds it: at 128, the chain of one row tile (scores 540 cycles,
 // maximum 570, weights 1,750, product 870, hand-overs 700) against the other's, with the SM issuing
 // 44% of the time; at 256 conversion and products about equally (without conversion 1.61 ms, with a
 // quarter of the products 1.82 ms).  Tried without gain: four softmax groups of half a row each
@@ -222,36 +222,43 @@ __global__ void __launch_bounds__(PromptShape<D>::THREADS, 1)
     const Seq s = load_seq(B, b, a.hdr);
     return (s.n * a.group + P::ROWS - 1) / P::ROWS;
   };
+  // inclusive sum over the block of each thread's n; adds the block's total to `total`
   int total = 0;
-  for (int b0 = 0; b0 < B.batch; b0 += P::THREADS) {
-    const int n = __reduce_add_sync(~0u, tiles_of(b0 + tid));
-    if (lane == 0) s_count[warp] = n;
+  auto scan = [&](int n) {
+    int sum = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int up = __shfl_up_sync(~0u, sum, o);
+      if (lane >= o) sum += up;
+    }
+    if (lane == 31) s_count[warp] = sum;
     __syncthreads();
-    for (int w = 0; w < WARPS; ++w) total += s_count[w];
+    int before = total;
+    for (int w = 0; w < WARPS; ++w) {
+      if (w < warp) before += s_count[w];
+      total += s_count[w];
+    }
     __syncthreads();
-  }
+    return before + sum;
+  };
+  const int n_first = tiles_of(tid), sum_first = scan(n_first);
+  for (int b0 = P::THREADS; b0 < B.batch; b0 += P::THREADS) scan(tiles_of(b0 + tid));
   const int h = blockIdx.x % a.kv_heads, want = total - 1 - (int)(blockIdx.x / a.kv_heads);
   const int split = blockIdx.y;
-  int before = 0;
+  auto look = [&](int b, int n, int sum) {
+    if (want < sum && want >= sum - n) {
+      s_found[0] = b;
+      s_found[1] = want - (sum - n);
+    }
+  };
   if (want >= 0) {
-    for (int b0 = 0; b0 < B.batch; b0 += P::THREADS) {
-      const int n = tiles_of(b0 + tid);
-      int sum = n;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int up = __shfl_up_sync(~0u, sum, o);
-        if (lane >= o) sum += up;
+    look(tid, n_first, sum_first);
+    if (B.batch > P::THREADS) {
+      total = 0;
+      for (int b0 = 0; b0 < B.batch; b0 += P::THREADS) {
+        const int n = tiles_of(b0 + tid), sum = scan(n);
+        if (b0 > 0) look(b0 + tid, n, sum);
       }
-      if (lane == 31) s_count[warp] = sum;
-      __syncthreads();
-      for (int w = 0; w < warp; ++w) sum += s_count[w];
-      sum += before;
-      if (want < sum && want >= sum - n) {
-        s_found[0] = b0 + tid;
-        s_found[1] = want - (sum - n);
-      }
-      for (int w = 0; w < WARPS; ++w) before += s_count[w];
-      __syncthreads();
     }
   }
   __syncthreads();
@@ -297,35 +304,39 @@ __global__ void __launch_bounds__(PromptShape<D>::THREADS, 1)
     const int64_t row = it.row0 + tok;
     float qf = 0.f;
     {
-      const uint4 *src = reinterpret_cast<const uint4 *>(a.q + row * a.q_ts + (int64_t)head * a.q_hs);
-      float top = 0.f;
-      if (live) {
-#pragma unroll 4
-        for (int c = 0; c < D / 8; ++c) {
-          float f[8];
-          if (bf16) unpack8<Bf16>(src[c], f);
-          else unpack8<F16>(src[c], f);
+      // a row's words all at once (head_dim 256: half of them in each group, which exchange maxima)
+      constexpr int WORDS = NQ == 2 ? D / 8 : D / 16;
+      const int c0 = NQ == 2 ? 0 : wg * WORDS;
+      const uint4 *src = reinterpret_cast<const uint4 *>(a.q + row * a.q_ts + (int64_t)head * a.q_hs) + c0;
+      uint4 raw[WORDS];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(f[i]));
-        }
+      for (int c = 0; c < WORDS; ++c) raw[c] = live ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
+      float top = 0.f;
+#pragma unroll
+      for (int c = 0; c < WORDS; ++c) {
+        float f[8];
+        if (bf16) unpack8<Bf16>(raw[c], f);
+        else unpack8<F16>(raw[c], f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(f[i]));
+      }
+      if (NQ == 1) {
+        s_ml[wg][r].x = top;
+        asm volatile("bar.sync 2, 256;" ::: "memory");
+        top = fmaxf(top, s_ml[wg ^ 1][r].x);
       }
       const int e = top > 0.f ? min(max(ilogbf(top), -100), 100) : 14;
       const float up = copysignf(__uint_as_float((uint32_t)(127 + 14 - e) << 23), a.scale2);
       qf = __uint_as_float((uint32_t)(127 - 14 + e) << 23) * fabsf(a.scale2);
       uint8_t *dst = mem + (NQ == 2 ? wg * P::TILE : 0);
-      const int c0 = NQ == 2 ? 0 : wg * (D / 16), c1 = NQ == 2 ? D / 8 : c0 + D / 16;
-#pragma unroll 4
-      for (int c = c0; c < c1; ++c) {
-        uint4 w = make_uint4(0, 0, 0, 0);
-        if (live) {
-          float f[8];
-          if (bf16) unpack8<Bf16>(src[c], f);
-          else unpack8<F16>(src[c], f);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) f[i] *= up;
-          w = pack8<F16>(f);
-        }
-        *reinterpret_cast<uint4 *>(dst + (c >> 3) * (kRows * 128) + tc::sw128(r, c & 7)) = w;
+      for (int c = 0; c < WORDS; ++c) {
+        float f[8];
+        if (bf16) unpack8<Bf16>(raw[c], f);
+        else unpack8<F16>(raw[c], f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] *= up;
+        *reinterpret_cast<uint4 *>(dst + ((c0 + c) >> 3) * (kRows * 128) + tc::sw128(r, (c0 + c) & 7)) = pack8<F16>(f);
       }
       tc::fence_proxy_async();
     }
@@ -841,7 +852,10 @@ PromptPlan prompt_plan(const lily_kv8_cache &C, const lily_kv8_batch &b, int T, 
   const int sms = sm_count() > 0 ? sm_count() : 152;
   const int64_t tiles = (b.max_kv + 16LL + kKeys - 1) / kKeys;
   // Few row tiles: the keys are split too, so that every SM has a share, of four tiles at least (a
-  // share costs its block's start and a write and read of its output).
+  // share costs its block's start and a write and read of its output).  More shares than SMs, to even out
+  // ragged lengths, were slower: 9 sequences of 49 tokens after up to 42,909, 5 heads of 128: 66 us with
+  // one share an SM, 67, 73 and 86 with two, three and four; 379 tokens after 64,380, 8 heads of 64: 92,
+  // 100, 110, 119.
   p.items = (int)items;
   p.splits = (int)std::max<int64_t>(1, std::min<int64_t>(sms / items, tiles / 4));
   // The space is that of sms parts, which any number of row tiles keeps to, so that a workspace
