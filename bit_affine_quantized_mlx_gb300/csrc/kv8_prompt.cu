@@ -222,43 +222,36 @@ __global__ void __launch_bounds__(PromptShape<D>::THREADS, 1)
     const Seq s = load_seq(B, b, a.hdr);
     return (s.n * a.group + P::ROWS - 1) / P::ROWS;
   };
-  // inclusive sum over the block of each thread's n; adds the block's total to `total`
   int total = 0;
-  auto scan = [&](int n) {
-    int sum = n;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int up = __shfl_up_sync(~0u, sum, o);
-      if (lane >= o) sum += up;
-    }
-    if (lane == 31) s_count[warp] = sum;
+  for (int b0 = 0; b0 < B.batch; b0 += P::THREADS) {
+    const int n = __reduce_add_sync(~0u, tiles_of(b0 + tid));
+    if (lane == 0) s_count[warp] = n;
     __syncthreads();
-    int before = total;
-    for (int w = 0; w < WARPS; ++w) {
-      if (w < warp) before += s_count[w];
-      total += s_count[w];
-    }
+    for (int w = 0; w < WARPS; ++w) total += s_count[w];
     __syncthreads();
-    return before + sum;
-  };
-  const int n_first = tiles_of(tid), sum_first = scan(n_first);
-  for (int b0 = P::THREADS; b0 < B.batch; b0 += P::THREADS) scan(tiles_of(b0 + tid));
+  }
   const int h = blockIdx.x % a.kv_heads, want = total - 1 - (int)(blockIdx.x / a.kv_heads);
   const int split = blockIdx.y;
-  auto look = [&](int b, int n, int sum) {
-    if (want < sum && want >= sum - n) {
-      s_found[0] = b;
-      s_found[1] = want - (sum - n);
-    }
-  };
+  int before = 0;
   if (want >= 0) {
-    look(tid, n_first, sum_first);
-    if (B.batch > P::THREADS) {
-      total = 0;
-      for (int b0 = 0; b0 < B.batch; b0 += P::THREADS) {
-        const int n = tiles_of(b0 + tid), sum = scan(n);
-        if (b0 > 0) look(b0 + tid, n, sum);
+    for (int b0 = 0; b0 < B.batch; b0 += P::THREADS) {
+      const int n = tiles_of(b0 + tid);
+      int sum = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int up = __shfl_up_sync(~0u, sum, o);
+        if (lane >= o) sum += up;
       }
+      if (lane == 31) s_count[warp] = sum;
+      __syncthreads();
+      for (int w = 0; w < warp; ++w) sum += s_count[w];
+      sum += before;
+      if (want < sum && want >= sum - n) {
+        s_found[0] = b0 + tid;
+        s_found[1] = want - (sum - n);
+      }
+      for (int w = 0; w < WARPS; ++w) before += s_count[w];
+      __syncthreads();
     }
   }
   __syncthreads();
