@@ -8,10 +8,10 @@
 // float (8 or 11 significant bits), so 127 x and q amax are exact in fp32 (at most 18 bits).  Let
 // the numerator be an integer times 2^a and amax an integer N < 2^11 times 2^b: a quotient that is
 // not an odd multiple of 1/2 differs from every such multiple by at least 2^(a-b) / (2 N), and one
-// of 1/2 or more has 2^(a-b) >= 2^-9 or so: by 4e-7 at least.  the product with a rounded
-// 127 / amax is off by 2^-22 relative (3e-5 at most), so it decides everything farther than 1e-4 from a
-// tie; nearer, an IEEE
-// division (3e-8 off at 1/2, 2^-24 relative above) decides, and gives an exact tie exactly.
+// of 1/2 or more has 2^(a-b) >= 2^-9 or so: by 4e-7 at least.  The product with a rounded
+// 127 / amax is off by 2^-22 relative (3e-5 at most), so it decides everything farther than 1e-4
+// from a tie; nearer, an IEEE division (3e-8 off at 1/2, 2^-24 relative above) decides, and gives an
+// exact tie exactly.
 //
 // Bound by memory: 2 bytes in and 1 byte out an element; at one token a sequence by the launch
 // and one chain of dependent reads (lengths, page number, magnitude).  A run is read once, held

@@ -344,7 +344,7 @@ LILY_Q4_API int lily_qk_norm_rope(const lily_qk_rope *op, int32_t T, int32_t q_h
  * codes 16-byte aligned. */
 typedef struct {
   int8_t *k, *v;          /* [n_pages][kv_heads][page][head_dim] */
-  float *k_amax, *v_amax; /* [n_pages][kv_heads], finite and not negative */
+  float *k_amax, *v_amax; /* [n_pages][kv_heads], not negative (lily_kv8_append: a 16-bit float's value) */
   int32_t n_pages;
   int32_t kv_heads;
   int32_t page;     /* 16, 32, 64 or 128 */
