@@ -34,9 +34,9 @@
 // fp16 (2^-11 relative down to 2^-14, 2^-25 absolute below: relative to the largest term that any
 // one key adds to the output) and multiplies the codes; the softmax's sum adds 2^(x - max) / a in fp32.
 //
-// Measured on one GB300: 64 sequences of up to 32,768 tokens (1.12M in all), 32 / 8 heads of 128: 353 us
-// (6.5 TB/s of codes, 96% of the measured copy rate); one sequence of 262,144 tokens, 16 / 2 heads of 256:
-// 52 us with the join (5.2 TB/s, 76%: two blocks an SM, and 8 us of join); one of 777 tokens: 9 us, the
+// Measured on one GB300: 64 sequences of up to 32,768 tokens (1.12M in all), 32 / 8 heads of 128: 349 us
+// (6.6 TB/s of codes, 97% of the measured copy rate); one sequence of 262,144 tokens, 16 / 2 heads of 256:
+// 50.5 us with the join (5.3 TB/s, 78%: two blocks an SM, and 8 us of join); one of 777 tokens: 7.6 us, the
 // chain of dependent reads (lengths, pages, codes, parts) of two launches.
 #include <algorithm>
 
