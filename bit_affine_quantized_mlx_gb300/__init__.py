@@ -495,25 +495,35 @@ class QKNormRope:
 def lily_qk_norm_rope(op: QKNormRope, q, k, pos, q_out, k_out, stream=None):
     """Norm and rotation of every head of q [T, q_heads, D] and k [T, k_heads, D] (views with any
     token and head strides) into q_out and k_out, which may be q and k; k may be None."""
-    T, hq, d = q.shape
+    shape, t = q.shape, q.dtype
+    if len(shape) != 3:
+        raise Q4Error(ERR_INVALID_ARG, f"lily_qk_norm_rope: q {tuple(shape)}")
+    T, hq, d = shape
     dtype = _dtype_code(q, "lily_qk_norm_rope")
-    t = q.dtype
-    if q_out.dtype is not t or (k is not None and (k.dtype is not t or k_out.dtype is not t)):
-        raise Q4Error(ERR_INVALID_ARG, "lily_qk_norm_rope: q, k and their outputs of one type")
-    if d != op.head_dim:
-        raise Q4Error(ERR_INVALID_ARG, f"lily_qk_norm_rope: heads of {d}")
-    hk, kr, ko = 0, (0, 0, 0), (0, 0, 0)
-    if k is not None:
+    if q_out.shape != shape or q_out.dtype is not t or d != op.head_dim:
+        raise Q4Error(ERR_INVALID_ARG, f"lily_qk_norm_rope: q {tuple(shape)}, q_out {tuple(q_out.shape)}, "
+                                       f"{t}, {q_out.dtype}, heads of {op.head_dim}")
+    qi, qo = q.stride(), q_out.stride()
+    if (qi[2] != 1 or qo[2] != 1) and q.numel():
+        raise Q4Error(ERR_INVALID_ARG, f"lily_qk_norm_rope: strides {qi}, {qo}")
+    if k is None:
+        hk, words = 0, (0, 0, 0, 0, 0, 0)
+    else:
         hk = k.shape[1]
-        kr, ko = _rows(k, T, hk, d, "k"), _rows(k_out, T, hk, d, "k_out")
+        if k.shape != (T, hk, d) or k_out.shape != k.shape or k.dtype is not t or k_out.dtype is not t:
+            raise Q4Error(ERR_INVALID_ARG, f"lily_qk_norm_rope: k {tuple(k.shape)}, k_out {tuple(k_out.shape)}, "
+                                           f"{k.dtype}, {k_out.dtype}")
+        ki, ko = k.stride(), k_out.stride()
+        if (ki[2] != 1 or ko[2] != 1) and k.numel():
+            raise Q4Error(ERR_INVALID_ARG, f"lily_qk_norm_rope: strides {ki}, {ko}")
+        words = (k.data_ptr(), ki[0], ki[1], k_out.data_ptr(), ko[0], ko[1])
     at = 0
     if op.rotary_dim:
         at = _int32(pos, "pos")
         if pos.numel() != T:
             raise Q4Error(ERR_INVALID_ARG, "lily_qk_norm_rope: pos")
-    rc = _call(0, _ROPE(op.c(dtype), T, hq, hk, at, *_rows(q, T, hq, d, "q"),
-                        *_rows(q_out, T, hq, d, "q_out"), *kr, *ko,
-                        _raw_stream(q.get_device()) if stream is None else stream.cuda_stream))
+    rc = _call(0, _ROPE(op.c(dtype), T, hq, hk, at, q.data_ptr(), qi[0], qi[1], q_out.data_ptr(), qo[0], qo[1],
+                        *words, _raw_stream(q.get_device()) if stream is None else stream.cuda_stream))
     return rc if rc == OK else _check(rc, "lily_qk_norm_rope")
 
 
@@ -600,17 +610,23 @@ def lily_kv8_attention(cache: KV8Cache, batch: KV8Batch, q, out, scale, lse=None
                        window=0, ws=None, stream=None):
     """Attention of q [T, q_heads, head_dim] over the batch's cached tokens into out (same shape)
     and, if given, lse fp32 [T, q_heads]; see include/lily_q4.h."""
-    T, heads, d = q.shape
+    shape, t = q.shape, q.dtype
+    if len(shape) != 3:
+        raise Q4Error(ERR_INVALID_ARG, f"lily_kv8_attention: q {tuple(shape)}")
+    T, heads, d = shape
     dtype = _dtype_code(q, "lily_kv8_attention")
-    if out.dtype is not q.dtype or d != cache.head_dim:
-        raise Q4Error(ERR_INVALID_ARG, "lily_kv8_attention: q and out of one type, the cache's head_dim")
+    if out.shape != shape or out.dtype is not t or d != cache.head_dim:
+        raise Q4Error(ERR_INVALID_ARG, f"lily_kv8_attention: q {tuple(shape)}, out {tuple(out.shape)}, {t}, "
+                                       f"{out.dtype}, heads of {cache.head_dim}")
+    qi, qo = q.stride(), out.stride()
+    if (qi[2] != 1 or qo[2] != 1) and q.numel():
+        raise Q4Error(ERR_INVALID_ARG, f"lily_kv8_attention: strides {qi}, {qo}")
     at = 0
     if lse is not None:
         if lse.shape != (T, heads) or lse.dtype is not _float32_t or not lse.is_contiguous():
             raise Q4Error(ERR_INVALID_ARG, "lily_kv8_attention: lse is fp32 [T, q_heads]")
         at = lse.data_ptr()
     rc = _call(3, _ATTENTION(cache._at, batch._at, T, heads, dtype, scale, 1 if causal else 0, window,
-                             *_rows(q, T, heads, d, "q"), *_rows(out, T, heads, d, "out"), at,
-                             *_space(ws),
+                             q.data_ptr(), qi[0], qi[1], out.data_ptr(), qo[0], qo[1], at, *_space(ws),
                              _raw_stream(q.get_device()) if stream is None else stream.cuda_stream))
     return rc if rc == OK else _check(rc, "lily_kv8_attention")

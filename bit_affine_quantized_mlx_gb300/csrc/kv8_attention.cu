@@ -161,9 +161,12 @@ __global__ void __launch_bounds__(kDecThreads, decode_blocks(D, NT)) kv8_decode_
   }
   __syncthreads();
   // equal shares of the work; with less of it than blocks the last blocks have none
-  const int64_t total = s_pre[B.batch], G = min((int64_t)gridDim.x, total);
+  const uint32_t total = s_pre[B.batch], G = min(gridDim.x, total);
   if (blockIdx.x >= G) return;
-  const int begin = (int)(total * blockIdx.x / G), end = (int)(total * (blockIdx.x + 1) / G);
+  // floor(c total / G) in 32 bits: c (total mod G) is below 2^18
+  const uint32_t whole_share = total / G, rest = total - whole_share * G;
+  const int begin = blockIdx.x * whole_share + blockIdx.x * rest / G;
+  const int end = (blockIdx.x + 1) * whole_share + (blockIdx.x + 1) * rest / G;
 
   uint8_t *ring = smem + warp * RING;
   const uint32_t ring_u32 = tc::smem_u32(ring);
@@ -484,6 +487,7 @@ __global__ void __launch_bounds__(kDecThreads, decode_blocks(D, NT)) kv8_decode_
         den += s_l[w * RT + tid] * (mw == -INFINITY ? 1.f : ex2(mw - top));
       }
       s_fin[tid] = make_float2(top, den);
+      s_qf[tid] = den == 0.f ? 0.f : 1.f / (127.f * den);  // q's factors are not needed any more
     }
 #pragma unroll
     for (int n = 0; n < NT; ++n)
@@ -503,11 +507,10 @@ __global__ void __launch_bounds__(kDecThreads, decode_blocks(D, NT)) kv8_decode_
     __syncthreads();
     const bool split = t0 > 0 || t1 < ntile;
     const int slot = 2 * blockIdx.x + (cur == begin ? 0 : 1);
+#pragma unroll 8
     for (int e = tid; e < RT * (D / 2); e += kDecThreads) {
       const int r = e / (D / 2), d = (e - r * (D / 2)) * 2;
       const int2 ro = s_row[r];
-      if (ro.x < 0) continue;
-      const float2 fin = s_fin[r];
       float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
       for (int w = 0; w < kDecWarps; ++w) {
@@ -516,22 +519,27 @@ __global__ void __launch_bounds__(kDecThreads, decode_blocks(D, NT)) kv8_decode_
         sum.x += u.x;
         sum.y += u.y;
       }
+      if (ro.x < 0) continue;
       if (split) {
         *reinterpret_cast<float2 *>(a.part + ((int64_t)slot * RT + r) * D + d) = sum;
-        if (d == 0) a.ml[slot * RT + r] = fin;
       } else {
-        const float f = fin.y == 0.f ? 0.f : 1.f / (127.f * fin.y);
+        const float f = s_qf[r];
         const uint32_t w = bf16 ? Bf16::from_f32x2(sum.x * f, sum.y * f) : F16::from_f32x2(sum.x * f, sum.y * f);
         *reinterpret_cast<uint32_t *>(a.out + (int64_t)ro.x * a.o_ts + (int64_t)ro.y * a.o_hs + d) = w;
-        if (d == 0 && a.lse)
-          a.lse[(int64_t)ro.x * a.kv_heads * a.group + ro.y] =
-              fin.y == 0.f ? -INFINITY : (fin.x + log2f(fin.y)) * 0.69314718056f;
       }
+    }
+    if (tid < RT && s_row[tid].x >= 0) {
+      const float2 fin = s_fin[tid];
+      if (split)
+        a.ml[slot * RT + tid] = fin;
+      else if (a.lse)
+        a.lse[(int64_t)s_row[tid].x * a.kv_heads * a.group + s_row[tid].y] =
+            fin.y == 0.f ? -INFINITY : (fin.x + log2f(fin.y)) * 0.69314718056f;
     }
     if (split && t0 == 0 && tid == 0) {
       // the block that holds the item's last tile: the largest c with floor(c total / G) <= it
       const int64_t last = cur - u0 + per - 1;
-      const int c_last = (int)(((last + 1) * G - 1) / total);
+      const int c_last = (int)(((last + 1) * G - 1) / (int64_t)total);
       a.jobs[2 * blockIdx.x] = make_int4(sq.row0, sq.n, h, rt);
       a.jobs[2 * blockIdx.x + 1] = make_int4(slot, c_last, 0, 0);
     }
