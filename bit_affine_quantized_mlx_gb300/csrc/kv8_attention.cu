@@ -738,7 +738,7 @@ size_t kv8_attention_ws_bytes(const lily_kv8_cache &C, const lily_kv8_batch &b, 
   if (!prompt_form(C, b, q_heads)) return decode_plan(C, b, T, q_heads).total;
   lily_kv8_batch fewer = b;  // the split form's largest calls, so that the space serves them too
   fewer.max_q = std::max(1, 96 / (q_heads / C.kv_heads));
-  return std::max(decode_plan(C, fewer, T, q_heads).total, prompt_plan(C, b, T, q_heads).total);
+  return std::max(decode_plan(C, fewer, T, q_heads).total, prompt_plan(C, b, T, q_heads, 0).total);
 }
 
 int launch_kv8_attention(const lily_kv8_cache &C, const lily_kv8_batch &b, const AttnShape &s,
@@ -766,7 +766,7 @@ int launch_kv8_attention(const lily_kv8_cache &C, const lily_kv8_batch &b, const
   const int bf16 = s.dtype == LILY_BF16;
   cudaError_t e;
   if (prompt_form(C, b, s.q_heads)) {
-    e = launch_prompt(a, prompt_plan(C, b, s.T, s.q_heads), C.head_dim, bf16, w, st);
+    e = launch_prompt(a, prompt_plan(C, b, s.T, s.q_heads, s.window), C.head_dim, bf16, w, st);
     if (e == cudaSuccess) return LILY_Q4_OK;
     cudaGetLastError();
     return LILY_Q4_ERR_CUDA;

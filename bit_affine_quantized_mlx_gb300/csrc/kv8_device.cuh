@@ -146,7 +146,8 @@ struct PromptPlan {
   int items, splits;  // row tiles times key/value heads (a bound), parts of their keys
   size_t off_jobs, off_ml, off_part, total;  // total 0: too many items
 };
-PromptPlan prompt_plan(const lily_kv8_cache &C, const lily_kv8_batch &b, int T, int q_heads);
+// The offsets and the total do not depend on the window.
+PromptPlan prompt_plan(const lily_kv8_cache &C, const lily_kv8_batch &b, int T, int q_heads, int window);
 cudaError_t launch_prompt(const AttnArgs &args, const PromptPlan &p, int D, int bf16, uint8_t *ws,
                           cudaStream_t st);
 

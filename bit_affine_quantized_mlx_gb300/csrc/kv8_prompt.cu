@@ -29,7 +29,7 @@
 //
 // Measured on one GB300: 5 ragged prompts, 6.6k tokens over up to 8k keys each, 32 / 8 heads of 128: 649 us
 // (981 TFLOP/s, 51% of the measured bf16 rate); a 4096-token chunk after 28,672, 16 / 2 heads of 256:
-// 2.08 ms (990 TFLOP/s, 52%).  What bounds it: at 128, the chain of one row tile (scores 540 cycles,
+// 1.95 ms (1,058 TFLOP/s, 55%).  What bounds it: at 128, the chain of one row tile (scores 540 cycles,
 // maximum 570, weights 1,750, product 870, hand-overs 700) against the other's, with the SM issuing
 // 44% of the time; at 256 conversion and products about equally (without conversion 1.61 ms, with a
 // quarter of the products 1.82 ms).  Tried without gain: four softmax groups of half a row each
@@ -833,7 +833,7 @@ __global__ void __launch_bounds__(256) kv8_prompt_join_kernel(AttnArgs a, int bf
 }
 
 // ----------------------------------------------------------------------------- launches
-PromptPlan prompt_plan(const lily_kv8_cache &C, const lily_kv8_batch &b, int T, int q_heads) {
+PromptPlan prompt_plan(const lily_kv8_cache &C, const lily_kv8_batch &b, int T, int q_heads, int window) {
   PromptPlan p = {};
   const int64_t group = q_heads / C.kv_heads, D = C.head_dim;
   const int64_t R = kRows * (D == 256 ? 1 : 2);
@@ -843,23 +843,33 @@ PromptPlan prompt_plan(const lily_kv8_cache &C, const lily_kv8_batch &b, int T, 
   const int64_t items = std::max<int64_t>(1, rows) * C.kv_heads;
   if (items > INT32_MAX) return p;
   const int sms = sm_count() > 0 ? sm_count() : 152;
-  const int64_t tiles = (b.max_kv + 16LL + kKeys - 1) / kKeys;
-  // Few row tiles: the keys are split too, so that every SM has a share, of four tiles at least (a
-  // share costs its block's start and a write and read of its output).  More shares than SMs, to even out
-  // ragged lengths, were slower: 9 sequences of 49 tokens after up to 42,909, 5 heads of 128: 66 us with
-  // one share an SM, 67, 73 and 86 with two, three and four; 379 tokens after 64,380, 8 heads of 64: 92,
-  // 100, 110, 119.
+  // key tiles of a row tile, by the host's bounds
+  const int64_t all = (b.max_kv + 16LL + kKeys - 1) / kKeys, per_seq = (b.max_q * group + R - 1) / R * C.kv_heads;
+  const int64_t tiles = window ? std::min(all, (window + R / group + 17 + kKeys - 1) / kKeys + 1) : all;
+  // The keys are split too with few row tiles, so that every SM has a share, of two tiles at least
+  // (1568 tokens of one head in a window of 439: 30 us in shares of four tiles or more, 24 of two, 21 of
+  // one; 300 tokens of 32 / 8 heads: 17.5 of two, 22 of one); and where one sequence fills the SMs and the last round of blocks would leave most of them idle: 512 row
+  // tiles of 256 key tiles are four rounds on 152 SMs, the last a third full, and in halves seven rounds
+  // of half the length (2.08 -> 1.95 ms; a share costs its block's start and a write and read of its
+  // output, about four key tiles).  Otherwise ragged lengths even themselves out, and more shares
+  // than SMs were slower: 9 sequences of 49 tokens after up to 42,909, 5 heads of 128: 66 us with one
+  // share an SM, 67, 73 and 86 with two, three and four; 85 of 7 tokens after up to 2576, 32 / 2 heads
+  // of 256: 80 whole, 93 in halves.
+  const int64_t most = items < sms ? sms : 8 * sms;  // parts in the workspace
+  auto time = [&](int64_t n) { return (items * n + sms - 1) / sms * (tiles / (double)n + 4); };
   p.items = (int)items;
-  p.splits = (int)std::max<int64_t>(1, std::min<int64_t>(sms / items, tiles / 4));
-  // The space is that of sms parts, which any number of row tiles keeps to, so that a workspace
-  // serves smaller calls too.
+  p.splits = (int)std::max<int64_t>(1, std::min<int64_t>(sms / items, tiles / 2));
+  if (per_seq >= sms)
+    for (int64_t n = 2; n <= tiles / 4 && items * n <= most; ++n)
+      if (time(n) < 0.97 * time(p.splits)) p.splits = (int)n;
+  // The space is that of the most parts, so that a workspace serves smaller calls too.
   size_t off = kAlign;
   p.off_jobs = off;
-  off = align_up(off + sms * sizeof(int4));
+  off = align_up(off + most * sizeof(int4));
   p.off_ml = off;
-  off = align_up(off + sms * R * sizeof(float2));
+  off = align_up(off + most * R * sizeof(float2));
   p.off_part = off;
-  p.total = tiles >= 8 ? align_up(off + (size_t)sms * R * D * sizeof(float)) : kAlign;
+  p.total = all >= 4 ? align_up(off + (size_t)most * R * D * sizeof(float)) : kAlign;
   return p;
 }
 
