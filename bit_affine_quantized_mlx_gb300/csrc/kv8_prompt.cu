@@ -342,7 +342,13 @@ __global__ void __launch_bounds__(PromptShape<D>::THREADS, 1)
     const uint32_t t_row = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t t_s = t_row + 128 * wg, t_o = t_row + 256 + (NQ == 2 ? wg * D : 0);
     const uint32_t s_full_w = s_full + 8 * wg, p_full_w = p_full + 8 * wg;
-    const uint32_t pv_w = pv_done + (NQ == 2 ? 8 * wg : 0);
+    // The product of key tile j.  head_dim 256 has a barrier for each parity of j: the last wait
+    // may come while the last two products are both under way, and one barrier's parity would
+    // take the end of the product before them for that of the last.
+    auto wait_pv = [&](int j) {
+      return NQ == 2 ? wait_warp(pv_done + 8 * wg, j & 1, abort_flag, err)
+                     : wait_warp(pv_done + 8 * (j & 1), (j >> 1) & 1, abort_flag, err);
+    };
     constexpr int STEP = NQ == 2 ? 1 : 2;
     const int j_first = NQ == 2 ? 0 : wg, j_end = NQ == 2 && wg >= nq ? 0 : tiles;
     float m = -INFINITY, l = 0.f;
@@ -425,7 +431,7 @@ __global__ void __launch_bounds__(PromptShape<D>::THREADS, 1)
         if (NQ == 1) s_max[r] = m;
         if (j > 0) {
           // O is only touched between the product of the last tile and that of this one
-          if (!(ok = wait_warp(pv_w, (j - 1) & 1, abort_flag, err))) break;
+          if (!(ok = wait_pv(j - 1))) break;
           tc::tc_fence_after();
 #pragma unroll 1
           for (int c = 0; c < D / 32; ++c) {
@@ -477,7 +483,7 @@ __global__ void __launch_bounds__(PromptShape<D>::THREADS, 1)
       m = fmaxf(x.x, y.x);
       l = x.y * (x.x == -INFINITY ? 1.f : ex2_approx(x.x - m)) + y.y * (y.x == -INFINITY ? 1.f : ex2_approx(y.x - m));
     }
-    if (ok && j_end > 0) ok = wait_warp(pv_w, (j_end - 1) & 1, abort_flag, err);
+    if (ok && j_end > 0) ok = wait_pv(j_end - 1);
     tc::tc_fence_after();
     if (ok && it.n > 0 && (NQ == 1 || wg < nq)) {
       // the row saw nothing (O may not exist); a row of NaN has no maximum, but a sum of NaN
@@ -765,7 +771,7 @@ __global__ void __launch_bounds__(PromptShape<D>::THREADS, 1)
       if (tiles > 0) scores(0);
       for (int j = 0; j < tiles && ok; ++j) {
         if (j + 1 < tiles) {
-          if (j > 0) wait(pv_done, j - 1);  // that slot's weights have been used
+          if (j > 0) wait(pv_done + 8 * ((j - 1) & 1), (j - 1) >> 1);  // that slot's weights have been used
           scores(j + 1);
         }
         wait(p_full + 8 * (j & 1), j >> 1);
@@ -775,7 +781,7 @@ __global__ void __launch_bounds__(PromptShape<D>::THREADS, 1)
           pv(base + vAt, 0, j & 1, u, u + 1, j == 0);
           commit(v_free + 8 * u);
         }
-        commit(pv_done);
+        commit(pv_done + 8 * (j & 1));
       }
     }
     // nothing of this warp's products is in flight when the tensor memory is given back

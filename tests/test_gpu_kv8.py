@@ -294,6 +294,10 @@ ATTENTION = [
     ([0], [257], 1, 1, 128, 128, "float16", 0, True),
     ([64, 5], [200, 64], 1, 48, 64, 32, "bfloat16", 0, True),
     ([3], [5], 1, 128, 64, 16, "float16", 0, True),
+    ([1800], [310], 8, 8, 256, 64, "bfloat16", 0, True),    # one sequence fills the SMs: keys in halves
+    ([1000, 0], [64, 200], 1, 3, 128, 16, "float16", 300, True),  # few row tiles in a window
+    ([700], [97], 1, 1, 256, 32, "bfloat16", 0, True),      # heads of 256 from 97 rows, few sequences
+    ([700], [96], 1, 1, 256, 32, "bfloat16", 0, True),
 ]
 
 
@@ -344,6 +348,23 @@ def test_attention_repeats_bit_for_bit_and_on_another_stream(torch):
         a = check_attention(torch, s, 8, 0.1, q=q)
         b = check_attention(torch, s, 8, 0.1, q=q, stream=torch.cuda.Stream())
         assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+@pytest.mark.parametrize("D,tokens", [(256, 310), (128, 310), (64, 310), (256, 40)])
+def test_prompt_form_repeats_bit_for_bit(torch, D, tokens):
+    # many blocks at once, whose products and conversions end in another order each time
+    s = Setup(torch, [1800], [tokens], 8, D, 64, "float16", seed=D + tokens).upload()
+    q = s.rows(64, 1.5).cuda()
+    ws = q4.new_workspace(q4.lily_kv8_attention_workspace_bytes(s.cache, s.batch, s.T, 64))
+    runs = []
+    for _ in range(12):
+        out = torch.empty((s.T, 64, D), dtype=s.dt, device="cuda")
+        lse = torch.empty((s.T, 64), dtype=torch.float32, device="cuda")
+        q4.lily_kv8_attention(s.cache, s.batch, q, out, D ** -0.5, lse=lse, ws=ws)
+        runs.append((out, lse))
+    torch.cuda.synchronize()
+    for out, lse in runs[1:]:
+        assert torch.equal(out, runs[0][0]) and torch.equal(lse, runs[0][1])
 
 
 @pytest.mark.parametrize("new", [1, 33])
