@@ -618,9 +618,10 @@ __global__ void __launch_bounds__(PromptShape<D>::THREADS, 1)
     auto free_wait = [&](uint32_t b, int n) {
       return n == 0 || wait_warp(b, (n - 1) & 1, abort_flag, err);
     };
-    // The proxy fence between these stores and the products is the issuing warp's, after its wait: here
-    // it would wait for the loads of the next codes too (a half of V took 2,000 cycles instead of 500).
-    auto publish = [&](uint32_t b) { tc::mbar_arrive(b); };
+    auto publish = [&](uint32_t b) {
+      tc::fence_proxy_async();
+      tc::mbar_arrive(b);
+    };
     const int page0 = page_of(0, lane & 7);
     int page = page_of(1, lane & 7);
     if constexpr (NQ == 2) {
@@ -699,10 +700,6 @@ __global__ void __launch_bounds__(PromptShape<D>::THREADS, 1)
     asm volatile("bar.sync 1, 288;" ::: "memory");
     bool ok = true;
     auto wait = [&](uint32_t b, int phase) { ok = ok && wait_warp(b, phase & 1, abort_flag, err); };
-    auto wait_codes = [&](uint32_t b, int phase) {
-      wait(b, phase);
-      tc::fence_proxy_async();  // the converting warps' stores, for the products that read them
-    };
     // S slot = Q(q) K^T over the elements [64 first, 64 last) of a K buffer
     auto qk = [&](uint32_t sk, int q, int slot, int first, int last) {
       if (!ok) return;
@@ -732,7 +729,7 @@ __global__ void __launch_bounds__(PromptShape<D>::THREADS, 1)
     if constexpr (NQ == 2) {
       // the two row tiles take turns: while one's weights are computed the other's products run
       if (tiles > 0) {
-        wait_codes(k_full, 0);
+        wait(k_full, 0);
         for (int q = 0; q < nq; ++q) {
           qk(base + kAt, q, q, 0, D / 64);
           commit(s_full + 8 * q);
@@ -741,14 +738,14 @@ __global__ void __launch_bounds__(PromptShape<D>::THREADS, 1)
       }
       for (int j = 0; j < tiles && ok; ++j) {
         const int b = j & 1;
-        wait_codes(v_full + 8 * b, j >> 1);
+        wait(v_full + 8 * b, j >> 1);
         for (int q = 0; q < nq; ++q) {
           wait(p_full + 8 * q, j);
           pv(base + vAt + b * P::TILE, q, q, 0, 2, j == 0);
           commit(pv_done + 8 * q);
           if (q == nq - 1) commit(v_free + 8 * b);
           if (j + 1 < tiles) {
-            if (q == 0) wait_codes(k_full + 8 * (b ^ 1), (j + 1) >> 1);
+            if (q == 0) wait(k_full + 8 * (b ^ 1), (j + 1) >> 1);
             wait(pv_done + 8 * q, j);  // S takes the columns of P
             qk(base + kAt + (b ^ 1) * P::TILE, q, q, 0, D / 64);
             commit(s_full + 8 * q);
@@ -762,7 +759,7 @@ __global__ void __launch_bounds__(PromptShape<D>::THREADS, 1)
       auto scores = [&](int j) {
 #pragma unroll
         for (int i = 0; i < D / 64; ++i) {
-          wait_codes(k_full + 8 * i, j);
+          wait(k_full + 8 * i, j);
           qk(base + kAt, 0, j & 1, i, i + 1);
           commit(k_free + 8 * i);
         }
@@ -777,7 +774,7 @@ __global__ void __launch_bounds__(PromptShape<D>::THREADS, 1)
         wait(p_full + 8 * (j & 1), j >> 1);
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          wait_codes(v_full + 8 * u, j);
+          wait(v_full + 8 * u, j);
           pv(base + vAt, 0, j & 1, u, u + 1, j == 0);
           commit(v_free + 8 * u);
         }
