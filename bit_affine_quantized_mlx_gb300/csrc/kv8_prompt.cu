@@ -25,13 +25,19 @@
 // weight-times-magnitude (see kv8_attention.cu for the magnitudes' place in the exponent).
 //
 // The running maximum moves only when a row's grows by more than 2^8 (weights up to 256 are as exact
-// in fp16), because moving it rescales O in tensor memory.
+// in fp16), because moving it rescales O in tensor memory.  Head_dim 64 and 128 need no maximum before
+// the weights then: a tile is done in one pass to the maximum there is, and done again where a row has
+// grown by more than 2^14 (657 -> 647 us for the ragged prompts below; 607 us with registers for it).
+// The pass holds a row's 64 words of weights until it is known to stand, so the softmax warps take
+// registers from the issuing warp's group (160 each and 64; 168 and 40: 615 us; 176 and 24: 746 us;
+// 152 and 80: 631 us).
 //
-// Measured on one GB300: 5 ragged prompts, 6.6k tokens over up to 8k keys each, 32 / 8 heads of 128: 649 us
-// (981 TFLOP/s, 51% of the measured bf16 rate); a 4096-token chunk after 28,672, 16 / 2 heads of 256:
+// Measured on one GB300: 5 ragged prompts, 6.6k tokens over up to 8k keys each, 32 / 8 heads of 128: 607 us
+// (1,049 TFLOP/s, 55% of the measured bf16 rate); a 4096-token chunk after 28,672, 16 / 2 heads of 256:
 // 1.95 ms (1,058 TFLOP/s, 55%).  What bounds it: at 128, the chain of one row tile (scores 540 cycles,
-// maximum 570, weights 1,750, product 870, hand-overs 700) against the other's, with the SM issuing
-// 44% of the time; at 256 conversion and products about equally (without conversion 1.61 ms, with a
+// weights and maximum about 1,800, product 870, hand-overs 700) against the other's, and the issue of
+// the softmax's instructions (an eighth of the exponentials as polynomials instead: 657 -> 679 us, half
+// of them 748); at 256 conversion and products about equally (without conversion 1.61 ms, with a
 // quarter of the products 1.82 ms).  Tried without gain: four softmax groups of half a row each
 // (751 us), issuing whichever row tile is ready (886 us), starting the product after half of the
 // weights, longer suspension in barrier waits.
@@ -49,7 +55,9 @@ struct PromptShape {
   static constexpr int NQ = D == 256 ? 1 : 2;   // row tiles of a block
   static constexpr int KB = D == 256 ? 1 : 2;   // buffers of K and of V
   static constexpr int CW = D == 256 ? 8 : 4;   // converting warps
-  static constexpr int THREADS = 32 * (8 + CW + 1);
+  static constexpr int THREADS = 32 * (8 + CW + (D == 256 ? 1 : 4));
+  // Registers a thread after the split at head_dim 64, 128, of 128 at launch: 2 x 160 + 128 + 64 = 4 x 128
+  static constexpr int SOFTMAX_REGS = 160, ISSUE_REGS = 64;
   static constexpr int ROWS = kRows * NQ;
   static constexpr int TILE = kKeys * D * 2;    // bytes of a K or V tile (and of 128 rows of Q)
   static constexpr int VW = D == 64 ? 2 : 4;    // words of a token a lane holds of V
@@ -101,7 +109,7 @@ __device__ __forceinline__ void tm_ld16_wait(uint32_t *r) {
                : "memory");
 }
 // f(c, W columns) for each W-column part c of a row's 128, the next part's load under way.
-template <int W, typename F>
+template <int W, int UNROLL = W == 32 ? 2 : 1, typename F>
 __device__ __forceinline__ void for_columns(uint32_t addr, F f) {
   uint32_t x[W], y[W];
   auto start = [&](int c, uint32_t *r) {
@@ -115,7 +123,7 @@ __device__ __forceinline__ void for_columns(uint32_t addr, F f) {
   start(0, x);
   // Unrolled at 32 columns (five percent of the whole at head_dim 128); at 16, where a thread has
   // 96 registers, unrolling spills (half as fast again).
-#pragma unroll(W == 32 ? 2 : 1)
+#pragma unroll(UNROLL)
   for (int c = 0; c < 128 / W; c += 2) {
     wait(x);
     start(c + 1, y);
@@ -287,6 +295,7 @@ __global__ void __launch_bounds__(PromptShape<D>::THREADS, 1)
   };
 
   if (warp < 8) {
+    if (NQ == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(P::SOFTMAX_REGS));
     // ======================================================================== softmax
     // Group wg of four warps: head_dim 64, 128: row tile wg, every key tile; head_dim 256: the
     // key tiles of its parity.  Its scores are in S slot wg either way.
@@ -398,18 +407,56 @@ __global__ void __launch_bounds__(PromptShape<D>::THREADS, 1)
         __syncwarp();
         qe = 1.f;
       }
-      // maximum: of a 16-key group's raw scores, then its factor and magnitude
+      // the maximum of a 16-key group: of its raw scores, then its factor and magnitude
+      auto group_top = [&](const uint32_t *s, float4 mt, float &top) {
+        float t = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < 16; i += 2) t = max3(t, __uint_as_float(s[i]), __uint_as_float(s[i + 1]));
+        if (t > -INFINITY) top = fmaxf(top, fmaf(t, mt.x * qe, mt.y));
+      };
+      // its weights, and what they add to the sum
+      auto group_weights = [&](const uint32_t *s, float4 mt, float m0, uint32_t *p, float &l) {
+        const float f = mt.x * qe, off = mt.y - m0;
+        const uint64_t f2 = pack2(f, f), off2 = pack2(off, off);
+        uint64_t sum = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float2 e = unpack2(fma2(pack2(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), f2, off2));
+          const float x0 = ex2_approx(e.x), x1 = ex2_approx(e.y);
+          sum = add2(sum, pack2(x0, x1));
+          p[i] = F16::from_f32x2(x0, x1);
+        }
+        const float2 both = unpack2(sum);
+        l = fmaf(both.x + both.y, mt.z, l);
+      };
       float top = -INFINITY;
+      if (NQ == 2 && whole && j > 0) {
+        // One pass: the weights to the running maximum as it is, in registers, and the tile's maximum
+        // beside them.  Weights up to 2^14 are as exact in fp16 as those below 1; only where a row has
+        // grown by more does the warp do the tile again (its scores are still there).
+        const float m0 = m == -INFINITY ? 0.f : m;
+        uint32_t p[64];
+        float sum = l;
+        for_columns<16, 4>(t_s, [&](int c, const uint32_t *s) {
+          const float4 mt = meta[c];
+          group_top(s, mt, top);
+          group_weights(s, mt, m0, p + 8 * c, sum);
+        });
+        if (!__any_sync(~0u, top > m + 14.f)) {
+          l = sum;
+#pragma unroll
+          for (int i = 0; i < 64; i += 8) tm_st8(t_s + i, p + i);
+          tm_st_wait();
+          tc::tc_fence_before();
+          tc::mbar_arrive(p_full_w);
+          continue;
+        }
+        top = -INFINITY;
+      }
       for_columns<P::COLS>(t_s, [&](int c, const uint32_t *s) {
 #pragma unroll
-        for (int g = 0; g < P::COLS / 16; ++g) {
-          const float4 mt = meta[c * (P::COLS / 16) + g];
-          float t = -INFINITY;
-#pragma unroll
-          for (int i = 0; i < 16; i += 2)
-            t = max3(t, __uint_as_float(s[16 * g + i]), __uint_as_float(s[16 * g + i + 1]));
-          if (t > -INFINITY) top = fmaxf(top, fmaf(t, mt.x * qe, mt.y));
-        }
+        for (int g = 0; g < P::COLS / 16; ++g)
+          group_top(s + 16 * g, meta[c * (P::COLS / 16) + g], top);
       });
       // move the running maximum?  (the first tile sets it: O is not there yet)
       if (NQ == 1) {  // the other group's last tile has decided
@@ -453,21 +500,8 @@ __global__ void __launch_bounds__(PromptShape<D>::THREADS, 1)
       for_columns<P::COLS>(t_s, [&](int c, const uint32_t *s) {
         uint32_t p[P::COLS / 2];
 #pragma unroll
-        for (int g = 0; g < P::COLS / 16; ++g) {
-          const float4 mt = meta[c * (P::COLS / 16) + g];
-          const float f = mt.x * qe, off = mt.y - m0;
-          const uint64_t f2 = pack2(f, f), off2 = pack2(off, off);
-          uint64_t sum = 0;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float2 e = unpack2(fma2(pack2(__uint_as_float(s[16 * g + 2 * i]), __uint_as_float(s[16 * g + 2 * i + 1])), f2, off2));
-            const float x0 = ex2_approx(e.x), x1 = ex2_approx(e.y);
-            sum = add2(sum, pack2(x0, x1));
-            p[8 * g + i] = F16::from_f32x2(x0, x1);
-          }
-          const float2 both = unpack2(sum);
-          l = fmaf(both.x + both.y, mt.z, l);
-        }
+        for (int g = 0; g < P::COLS / 16; ++g)
+          group_weights(s + 16 * g, meta[c * (P::COLS / 16) + g], m0, p + 8 * g, l);
 #pragma unroll
         for (int i = 0; i < P::COLS / 2; i += 8) tm_st8(t_s + c * (P::COLS / 2) + i, p + i);
       });
@@ -697,95 +731,99 @@ __global__ void __launch_bounds__(PromptShape<D>::THREADS, 1)
     }
   } else {
     // ======================================================================== products
-    asm volatile("bar.sync 1, 288;" ::: "memory");
-    bool ok = true;
-    auto wait = [&](uint32_t b, int phase) { ok = ok && wait_warp(b, phase & 1, abort_flag, err); };
-    // S slot = Q(q) K^T over the elements [64 first, 64 last) of a K buffer
-    auto qk = [&](uint32_t sk, int q, int slot, int first, int last) {
-      if (!ok) return;
-      tc::tc_fence_after();
-      const uint32_t sq = base + q * P::TILE;
+    // the group of the issuing warp (three of its warps have no work) hands registers to the softmax
+    if (NQ == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(P::ISSUE_REGS));
+    if (warp == 8 + P::CW) {
+      asm volatile("bar.sync 1, 288;" ::: "memory");
+      bool ok = true;
+      auto wait = [&](uint32_t b, int phase) { ok = ok && wait_warp(b, phase & 1, abort_flag, err); };
+      // S slot = Q(q) K^T over the elements [64 first, 64 last) of a K buffer
+      auto qk = [&](uint32_t sk, int q, int slot, int first, int last) {
+        if (!ok) return;
+        tc::tc_fence_after();
+        const uint32_t sq = base + q * P::TILE;
 #pragma unroll
-      for (int ks = 4 * first; ks < 4 * last; ++ks) {
-        const uint32_t off = (ks >> 2) * (kKeys * 128) + (ks & 3) * 32;
-        tc::mma_bf16_warp(tmem + 128 * slot, tc::desc_k128_sw128(sq + off), tc::desc_k128_sw128(sk + off),
-                          idesc_f16(kKeys), ks > 0);
-      }
-    };
-    // O(q) += P slot V over the keys [64 first, 64 last) of a V buffer
-    auto pv = [&](uint32_t sv, int q, int slot, int first, int last, bool fresh) {
-      if (!ok) return;
-      tc::tc_fence_after();
-#pragma unroll
-      for (int ks = 4 * first; ks < 4 * last; ++ks) {
-        const uint32_t off = (ks >> 2) * (D * 128) + (ks & 3) * 32;
-        tc::mma_bf16_ts_warp(tmem + 256 + q * D, tmem + 128 * slot + 8 * ks, tc::desc_k128_sw128(sv + off),
-                             idesc_f16(D), !fresh || ks > 0);
-      }
-    };
-    auto commit = [&](uint32_t b) {
-      if (ok) tc::mma_commit_warp(b);
-    };
-    if constexpr (NQ == 2) {
-      // the two row tiles take turns: while one's weights are computed the other's products run
-      if (tiles > 0) {
-        wait(k_full, 0);
-        for (int q = 0; q < nq; ++q) {
-          qk(base + kAt, q, q, 0, D / 64);
-          commit(s_full + 8 * q);
+        for (int ks = 4 * first; ks < 4 * last; ++ks) {
+          const uint32_t off = (ks >> 2) * (kKeys * 128) + (ks & 3) * 32;
+          tc::mma_bf16_warp(tmem + 128 * slot, tc::desc_k128_sw128(sq + off), tc::desc_k128_sw128(sk + off),
+                            idesc_f16(kKeys), ks > 0);
         }
-        commit(k_free);
-      }
-      for (int j = 0; j < tiles && ok; ++j) {
-        const int b = j & 1;
-        wait(v_full + 8 * b, j >> 1);
-        for (int q = 0; q < nq; ++q) {
-          wait(p_full + 8 * q, j);
-          pv(base + vAt + b * P::TILE, q, q, 0, 2, j == 0);
-          commit(pv_done + 8 * q);
-          if (q == nq - 1) commit(v_free + 8 * b);
-          if (j + 1 < tiles) {
-            if (q == 0) wait(k_full + 8 * (b ^ 1), (j + 1) >> 1);
-            wait(pv_done + 8 * q, j);  // S takes the columns of P
-            qk(base + kAt + (b ^ 1) * P::TILE, q, q, 0, D / 64);
+      };
+      // O(q) += P slot V over the keys [64 first, 64 last) of a V buffer
+      auto pv = [&](uint32_t sv, int q, int slot, int first, int last, bool fresh) {
+        if (!ok) return;
+        tc::tc_fence_after();
+#pragma unroll
+        for (int ks = 4 * first; ks < 4 * last; ++ks) {
+          const uint32_t off = (ks >> 2) * (D * 128) + (ks & 3) * 32;
+          tc::mma_bf16_ts_warp(tmem + 256 + q * D, tmem + 128 * slot + 8 * ks, tc::desc_k128_sw128(sv + off),
+                               idesc_f16(D), !fresh || ks > 0);
+        }
+      };
+      auto commit = [&](uint32_t b) {
+        if (ok) tc::mma_commit_warp(b);
+      };
+      if constexpr (NQ == 2) {
+        // the two row tiles take turns: while one's weights are computed the other's products run
+        if (tiles > 0) {
+          wait(k_full, 0);
+          for (int q = 0; q < nq; ++q) {
+            qk(base + kAt, q, q, 0, D / 64);
             commit(s_full + 8 * q);
-            if (q == nq - 1) commit(k_free + 8 * (b ^ 1));
+          }
+          commit(k_free);
+        }
+        for (int j = 0; j < tiles && ok; ++j) {
+          const int b = j & 1;
+          wait(v_full + 8 * b, j >> 1);
+          for (int q = 0; q < nq; ++q) {
+            wait(p_full + 8 * q, j);
+            pv(base + vAt + b * P::TILE, q, q, 0, 2, j == 0);
+            commit(pv_done + 8 * q);
+            if (q == nq - 1) commit(v_free + 8 * b);
+            if (j + 1 < tiles) {
+              if (q == 0) wait(k_full + 8 * (b ^ 1), (j + 1) >> 1);
+              wait(pv_done + 8 * q, j);  // S takes the columns of P
+              qk(base + kAt + (b ^ 1) * P::TILE, q, q, 0, D / 64);
+              commit(s_full + 8 * q);
+              if (q == nq - 1) commit(k_free + 8 * (b ^ 1));
+            }
           }
         }
-      }
-    } else {
-      // the next tile's scores are computed under this one's softmax, in the other slot; K's atoms
-      // and V's halves are given back as soon as they have been read
-      auto scores = [&](int j) {
+      } else {
+        // the next tile's scores are computed under this one's softmax, in the other slot; K's atoms
+        // and V's halves are given back as soon as they have been read
+        auto scores = [&](int j) {
 #pragma unroll
-        for (int i = 0; i < D / 64; ++i) {
-          wait(k_full + 8 * i, j);
-          qk(base + kAt, 0, j & 1, i, i + 1);
-          commit(k_free + 8 * i);
-        }
-        commit(s_full + 8 * (j & 1));
-      };
-      if (tiles > 0) scores(0);
-      for (int j = 0; j < tiles && ok; ++j) {
-        if (j + 1 < tiles) {
-          if (j > 0) wait(pv_done + 8 * ((j - 1) & 1), (j - 1) >> 1);  // that slot's weights have been used
-          scores(j + 1);
-        }
-        wait(p_full + 8 * (j & 1), j >> 1);
+          for (int i = 0; i < D / 64; ++i) {
+            wait(k_full + 8 * i, j);
+            qk(base + kAt, 0, j & 1, i, i + 1);
+            commit(k_free + 8 * i);
+          }
+          commit(s_full + 8 * (j & 1));
+        };
+        if (tiles > 0) scores(0);
+        for (int j = 0; j < tiles && ok; ++j) {
+          if (j + 1 < tiles) {
+            if (j > 0) wait(pv_done + 8 * ((j - 1) & 1), (j - 1) >> 1);  // that slot's weights have been used
+            scores(j + 1);
+          }
+          wait(p_full + 8 * (j & 1), j >> 1);
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          wait(v_full + 8 * u, j);
-          pv(base + vAt, 0, j & 1, u, u + 1, j == 0);
-          commit(v_free + 8 * u);
+          for (int u = 0; u < 2; ++u) {
+            wait(v_full + 8 * u, j);
+            pv(base + vAt, 0, j & 1, u, u + 1, j == 0);
+            commit(v_free + 8 * u);
+          }
+          commit(pv_done + 8 * (j & 1));
         }
-        commit(pv_done + 8 * (j & 1));
       }
+      // nothing of this warp's products is in flight when the tensor memory is given back
+      tc::mma_commit_warp(drain);
+      int left = 0;
+      tc::wait_bar(drain, 0, &left, err);
+      tc::tc_fence_before();
     }
-    // nothing of this warp's products is in flight when the tensor memory is given back
-    tc::mma_commit_warp(drain);
-    int left = 0;
-    tc::wait_bar(drain, 0, &left, err);
-    tc::tc_fence_before();
   }
   __syncthreads();
   if (warp == 0) tc::tmem_dealloc(tmem, 512);
@@ -851,8 +889,8 @@ PromptPlan prompt_plan(const lily_kv8_cache &C, const lily_kv8_batch &b, int T, 
   const int64_t tiles = window ? std::min(all, (window + R / group + 17 + kKeys - 1) / kKeys + 1) : all;
   // The keys are split too with few row tiles, so that every SM has a share, of two tiles at least
   // (1568 tokens of one head in a window of 439: 30 us in shares of four tiles or more, 24 of two, 21 of
-  // one; 300 tokens of 32 / 8 heads: 17.5 of two, 22 of one); and where one sequence fills the SMs and the last round of blocks would leave most of them idle: 512 row
-  // tiles of 256 key tiles are four rounds on 152 SMs, the last a third full, and in halves seven rounds
+  // one; 300 tokens of 32 / 8 heads: 17.5 of two, 22 of one); and where one sequence fills the SMs and
+  // the last round of blocks would leave most of them idle: 512 row tiles of 256 key tiles are four rounds on 152 SMs, the last a third full, and in halves seven rounds
   // of half the length (2.08 -> 1.95 ms; a share costs its block's start and a write and read of its
   // output, about four key tiles).  Otherwise ragged lengths even themselves out, and more shares
   // than SMs were slower: 9 sequences of 49 tokens after up to 42,909, 5 heads of 128: 66 us with one

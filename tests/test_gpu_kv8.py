@@ -341,6 +341,18 @@ def test_attention_large_and_small_queries(torch, new):
     check_attention(torch, s, 8, 0.125, q=q)
 
 
+@pytest.mark.parametrize("D,dtype", [(64, "float16"), (128, "bfloat16"), (256, "bfloat16")])
+@pytest.mark.parametrize("growth", [1.05, 1.4, 3.0])
+def test_prompt_form_growing_scores(torch, D, dtype, growth):
+    # the rows' maxima rise from one 128-key tile to the next, by less and by more than 2^14
+    s = Setup(torch, [1500], [70], 1, D, 128, dtype, seed=D)
+    own = s.table[0, :-(-int(s.len[0]) // 128)]
+    s.amax["k"][own, 0] = s.rounded(0.3 * np.minimum(growth ** np.arange(len(own)), 30.0))
+    q = s.rows(5)
+    q[:, 1] *= 0.05
+    check_attention(torch, s.upload(), 5, 0.5, q=q)
+
+
 def test_attention_repeats_bit_for_bit_and_on_another_stream(torch):
     for new in (1, 80):
         s = Setup(torch, [3000, 50, 700], [new] * 3, 2, 128, 32, "bfloat16").upload()
