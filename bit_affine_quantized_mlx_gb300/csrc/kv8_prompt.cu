@@ -26,16 +26,17 @@
 //
 // The running maximum moves only when a row's grows by more than 2^8 (weights up to 256 are as exact
 // in fp16), because moving it rescales O in tensor memory.  Head_dim 64 and 128 need no maximum before
-// the weights then: a tile is done in one pass to the maximum there is, and done again where a row has
-// grown by more than 2^14 (657 -> 647 us for the ragged prompts below; 607 us with registers for it).
-// The pass holds a row's 64 words of weights until it is known to stand, so the softmax warps take
-// registers from the issuing warp's group (160 each and 64; 168 and 40: 615 us; 176 and 24: 746 us;
-// 152 and 80: 631 us).
+// the weights then: a tile is done in one pass to the maximum there is, and done again where a row's
+// weights come to more than 2^15 (ragged prompts below: 657 us with a pass for the maximum, 608 with
+// the maximum beside the weights, 583 with their sum, which is there anyway, as the sign).  The pass
+// holds a row's 64 words of weights until it is known to stand, so the softmax warps take registers
+// from the issuing warp's group (160 a thread and 64; 168 and 40: 586 us; 152 and 80: 620 us; 144 and
+// 96: 609 us).  Head_dim 256 has no registers for it.
 //
-// Measured on one GB300: 5 ragged prompts, 6.6k tokens over up to 8k keys each, 32 / 8 heads of 128: 607 us
-// (1,049 TFLOP/s, 55% of the measured bf16 rate); a 4096-token chunk after 28,672, 16 / 2 heads of 256:
+// Measured on one GB300: 5 ragged prompts, 6.6k tokens over up to 8k keys each, 32 / 8 heads of 128: 583 us
+// (1,092 TFLOP/s, 57% of the measured bf16 rate); a 4096-token chunk after 28,672, 16 / 2 heads of 256:
 // 1.95 ms (1,058 TFLOP/s, 55%).  What bounds it: at 128, the chain of one row tile (scores 540 cycles,
-// weights and maximum about 1,800, product 870, hand-overs 700) against the other's, and the issue of
+// weights about 1,750, product 870, hand-overs 700) against the other's, and the issue of
 // the softmax's instructions (an eighth of the exponentials as polynomials instead: 657 -> 679 us, half
 // of them 748); at 256 conversion and products about equally (without conversion 1.61 ms, with a
 // quarter of the products 1.82 ms).  Tried without gain: four softmax groups of half a row each
@@ -414,7 +415,7 @@ __global__ void __launch_bounds__(PromptShape<D>::THREADS, 1)
         for (int i = 0; i < 16; i += 2) t = max3(t, __uint_as_float(s[i]), __uint_as_float(s[i + 1]));
         if (t > -INFINITY) top = fmaxf(top, fmaf(t, mt.x * qe, mt.y));
       };
-      // its weights, and what they add to the sum
+      // its weights, their sum, and what they add to the row's
       auto group_weights = [&](const uint32_t *s, float4 mt, float m0, uint32_t *p, float &l) {
         const float f = mt.x * qe, off = mt.y - m0;
         const uint64_t f2 = pack2(f, f), off2 = pack2(off, off);
@@ -428,21 +429,20 @@ __global__ void __launch_bounds__(PromptShape<D>::THREADS, 1)
         }
         const float2 both = unpack2(sum);
         l = fmaf(both.x + both.y, mt.z, l);
+        return both.x + both.y;
       };
-      float top = -INFINITY;
       if (NQ == 2 && whole && j > 0) {
-        // One pass: the weights to the running maximum as it is, in registers, and the tile's maximum
-        // beside them.  Weights up to 2^14 are as exact in fp16 as those below 1; only where a row has
-        // grown by more does the warp do the tile again (its scores are still there).
+        // One pass: the weights to the running maximum as it is, in registers.  Weights up to 2^15 are
+        // as exact in fp16 as those below 1, and none is more than their sum; only where a row's sum is
+        // more, or the row has no maximum yet, does the warp do the tile again (its scores are still
+        // there).  128 weights that come to more than 2^15 have one above 2^8: the maximum moves then.
         const float m0 = m == -INFINITY ? 0.f : m;
         uint32_t p[64];
-        float sum = l;
+        float sum = l, all = 0.f;
         for_columns<16, 4>(t_s, [&](int c, const uint32_t *s) {
-          const float4 mt = meta[c];
-          group_top(s, mt, top);
-          group_weights(s, mt, m0, p + 8 * c, sum);
+          all += group_weights(s, meta[c], m0, p + 8 * c, sum);
         });
-        if (!__any_sync(~0u, top > m + 14.f)) {
+        if (!__any_sync(~0u, all > 32768.f || m == -INFINITY)) {
           l = sum;
 #pragma unroll
           for (int i = 0; i < 64; i += 8) tm_st8(t_s + i, p + i);
@@ -451,8 +451,8 @@ __global__ void __launch_bounds__(PromptShape<D>::THREADS, 1)
           tc::mbar_arrive(p_full_w);
           continue;
         }
-        top = -INFINITY;
       }
+      float top = -INFINITY;
       for_columns<P::COLS>(t_s, [&](int c, const uint32_t *s) {
 #pragma unroll
         for (int g = 0; g < P::COLS / 16; ++g)
