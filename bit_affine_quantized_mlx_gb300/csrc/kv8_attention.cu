@@ -369,7 +369,7 @@ __global__ void __launch_bounds__(kDecThreads, decode_blocks(D, NT)) kv8_decode_
         const float ka = mt[j];
         float va = mt[NG + j];
         va = va < 1e-30f ? 1e-30f : va;
-        iv[j] = __frcp_rn(va);
+        iv[j] = fminf(__frcp_rn(va), 2e30f);  // a number for a magnitude of NaN too: 0 times it is 0
         const float lv = __log2f(va);
         const int tk = tok0 + 16 * j;
         const bool whole = ka >= 0.f && tk >= all_lo && tk + 16 <= all_hi;

@@ -377,7 +377,9 @@ __global__ void __launch_bounds__(PromptShape<D>::THREADS, 1)
       const uint32_t turn = (NQ == 2 ? j : j >> 1) & 1;
       const float va = page < 0 ? 1.f : mag.y < 1e-30f ? 1e-30f : mag.y;
       const bool whole = !__any_sync(~0u, page < 0) && k0 >= all_lo && k0 + kKeys <= all_hi;
-      if (lane < 8) meta[lane] = make_float4(page < 0 ? -1.f : mag.x, __log2f(va), __frcp_rn(va), 0.f);
+      // the reciprocal is a number for a magnitude of NaN too: a hidden key's weight of 0 times it is 0, and
+      // the rows that see the page have its NaN from the logarithm
+      if (lane < 8) meta[lane] = make_float4(page < 0 ? -1.f : mag.x, __log2f(va), fminf(__frcp_rn(va), 2e30f), 0.f);
       page = check_page(B, raw, a.hdr);
       mag = load_mag(page);
       raw = page_of(j + 2 * STEP, lane & 7);

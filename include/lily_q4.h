@@ -35,7 +35,8 @@
  *    256-byte aligned, zero-filled once before its first use (lily_q4_workspace_init
  *    or a memset).  The calls leave it reusable; they never need it cleared again.
  *  - Results are deterministic: no floating-point atomics touch an output.
- *  - NaN/Inf inputs are outside the contract (results unspecified).
+ *  - NaN/Inf inputs are outside the contract (results unspecified), but for the attention
+ *    operators, which say below how far they reach.
  */
 #ifndef LILY_Q4_H
 #define LILY_Q4_H
@@ -282,7 +283,9 @@ LILY_Q4_API int lily_q4_selftest_timeout(void *ws, size_t ws_bytes, int32_t whic
  *    strides are multiples of 8 (of 4 for fp32).
  *  - dtype: LILY_BF16 or LILY_F16 (and LILY_F32 where a call says so).
  *  - No head or token count is fixed; T == 0 returns LILY_Q4_OK and enqueues nothing.
- *  - Non-finite inputs stay where they are (a head, a page of one head, a row that reads it).
+ *  - Non-finite inputs stay where they are: a head of one token (rotation), a page of one head
+ *    (append, read), a row that sees a token of such a page or whose query is not finite (attention).
+ *    A token that is not finite makes its page so, for that head.
  */
 #define LILY_BF16 0
 #define LILY_F16 1
