@@ -30,9 +30,10 @@
 // weights are transposed into the second product's operand by movmatrix.
 //
 // Page magnitudes.  A page's key magnitude multiplies its scores.  Its value magnitude a enters the
-// exponent: x = s log2 e + log2 a, with the running maximum taken of x; 2^(x - max) <= 1 is rounded to
-// fp16 (2^-11 relative down to 2^-14, 2^-25 absolute below: relative to the largest term that any
-// one key adds to the output) and multiplies the codes; the softmax's sum adds 2^(x - max) / a in fp32.
+// exponent: x = s log2 e + log2 a, with the running reference m kept 14 below the largest x; 2^(x - m) <= 2^14
+// is rounded to fp16 (2^-11 relative down to 2^-28 of the largest, 2^-39 of it absolute below: of the largest
+// term that any one key adds to the output) and multiplies the codes; the softmax's sum adds 2^(x - m) / a in
+// fp32 (times a power of two, see kv8_device.cuh).
 //
 // Measured on one GB300: 64 sequences of up to 32,768 tokens (1.12M in all), 32 / 8 heads of 128: 349 us
 // (6.6 TB/s of codes, 97% of the measured copy rate); one sequence of 262,144 tokens, 16 / 2 heads of 256:
@@ -51,6 +52,8 @@ constexpr int kDecThreads = 128, kDecWarps = 4, kDecStages = 2;
 // fewer tiles (16 x 3 tokens over 4096 keys, 96 items of 17 tiles: 18.5 us without).
 constexpr int kStart = 2;
 constexpr int kTurnBytes = 4096;  // of keys, and of values, a warp and turn
+// The reference of a row's weights below its largest exponent: weights up to 2^14, and room for rounding, in fp16.
+constexpr int kBias = 14;
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -369,7 +372,7 @@ __global__ void __launch_bounds__(kDecThreads, decode_blocks(D, NT)) kv8_decode_
         const float ka = mt[j];
         float va = mt[NG + j];
         va = va < 1e-30f ? 1e-30f : va;
-        iv[j] = fminf(__frcp_rn(va), 2e30f);  // a number for a magnitude of NaN too: 0 times it is 0
+        iv[j] = fminf(__frcp_rn(va), 2e30f) * sum_scale(kBias);  // a number for a magnitude of NaN too: 0 times it is 0
         const float lv = __log2f(va);
         const int tk = tok0 + 16 * j;
         const bool whole = ka >= 0.f && tk >= all_lo && tk + 16 <= all_hi;
@@ -384,7 +387,7 @@ __global__ void __launch_bounds__(kDecThreads, decode_blocks(D, NT)) kv8_decode_
             top[n][qe] = fmaxf(top[n][qe], x);
           }
       }
-      // running maximum over the turn's tokens (lanes of equal t hold the same queries)
+      // running reference over the turn's tokens (lanes of equal t hold the same queries)
       bool grew = false;
 #pragma unroll
       for (int n = 0; n < NT; ++n)
@@ -393,6 +396,7 @@ __global__ void __launch_bounds__(kDecThreads, decode_blocks(D, NT)) kv8_decode_
 #pragma unroll
           for (int off = 4; off < 32; off <<= 1)
             top[n][e] = fmaxf(top[n][e], __shfl_xor_sync(~0u, top[n][e], off));
+          top[n][e] -= (float)kBias;
           grew |= top[n][e] > m[n][e];
         }
       if (__any_sync(~0u, grew)) {
@@ -487,7 +491,7 @@ __global__ void __launch_bounds__(kDecThreads, decode_blocks(D, NT)) kv8_decode_
         den += s_l[w * RT + tid] * (mw == -INFINITY ? 1.f : ex2(mw - top));
       }
       s_fin[tid] = make_float2(top, den);
-      s_qf[tid] = den == 0.f ? 0.f : 1.f / (127.f * den);  // q's factors are not needed any more
+      s_qf[tid] = den == 0.f ? 0.f : 1.f / den;  // q's factors are not needed any more
     }
 #pragma unroll
     for (int n = 0; n < NT; ++n)
@@ -524,7 +528,9 @@ __global__ void __launch_bounds__(kDecThreads, decode_blocks(D, NT)) kv8_decode_
         *reinterpret_cast<float2 *>(a.part + ((int64_t)slot * RT + r) * D + d) = sum;
       } else {
         const float f = s_qf[r];
-        const uint32_t w = bf16 ? Bf16::from_f32x2(sum.x * f, sum.y * f) : F16::from_f32x2(sum.x * f, sum.y * f);
+        sum.x = sum.x * out_scale(kBias) * f;
+        sum.y = sum.y * out_scale(kBias) * f;
+        const uint32_t w = bf16 ? Bf16::from_f32x2(sum.x, sum.y) : F16::from_f32x2(sum.x, sum.y);
         *reinterpret_cast<uint32_t *>(a.out + (int64_t)ro.x * a.o_ts + (int64_t)ro.y * a.o_hs + d) = w;
       }
     }
@@ -534,7 +540,7 @@ __global__ void __launch_bounds__(kDecThreads, decode_blocks(D, NT)) kv8_decode_
         a.ml[slot * RT + tid] = fin;
       else if (a.lse)
         a.lse[(int64_t)s_row[tid].x * a.kv_heads * a.group + s_row[tid].y] =
-            fin.y == 0.f ? -INFINITY : (fin.x + log2f(fin.y)) * 0.69314718056f;
+            fin.y == 0.f ? -INFINITY : row_lse(fin.x, fin.y, kBias);
     }
     if (split && t0 == 0 && tid == 0) {
       // the block that holds the item's last tile: the largest c with floor(c total / G) <= it
@@ -648,14 +654,15 @@ __global__ void __launch_bounds__(kJoinThreads) kv8_join_kernel(AttnArgs a, int 
       acc.z += u.z;
       acc.w += u.w;
     }
-    const float g = den == 0.f ? 0.f : 1.f / (127.f * den);
+    const float g = den == 0.f ? 0.f : 1.f / den;
+    acc = make_float4(acc.x * out_scale(kBias), acc.y * out_scale(kBias), acc.z * out_scale(kBias), acc.w * out_scale(kBias));
     uint2 w;
     w.x = bf16 ? Bf16::from_f32x2(acc.x * g, acc.y * g) : F16::from_f32x2(acc.x * g, acc.y * g);
     w.y = bf16 ? Bf16::from_f32x2(acc.z * g, acc.w * g) : F16::from_f32x2(acc.z * g, acc.w * g);
     *reinterpret_cast<uint2 *>(a.out + (int64_t)ro.row * a.o_ts + (int64_t)ro.head * a.o_hs + col * 4) = w;
     if (col == 0 && a.lse)
       a.lse[(int64_t)ro.row * a.kv_heads * a.group + ro.head] =
-          den == 0.f ? -INFINITY : (top + log2f(den)) * 0.69314718056f;
+          den == 0.f ? -INFINITY : row_lse(top, den, kBias);
   }
 }
 

@@ -151,6 +151,19 @@ PromptPlan prompt_plan(const lily_kv8_cache &C, const lily_kv8_batch &b, int T, 
 cudaError_t launch_prompt(const AttnArgs &args, const PromptPlan &p, int D, int bf16, uint8_t *ws,
                           cudaStream_t st);
 
+// Softmax weights.  fp16 has 15 octaves above 1 and loses what is below 2^-25, so a weight is
+// 2^(x - m) with the reference m `bias` below the largest x seen: the smallest that counts is then
+// 2^-(25 + bias) of the largest.  (With m the maximum itself, 262,144 keys 17.5 below one that carries little were
+// all lost from the output: 5% of it.)  The sum adds w 2^(6 - bias) / a, a the page's magnitude of values:
+// with a from 1e-30 to 3e38 and a million keys it and its reciprocal stay inside fp32's normal numbers.
+constexpr float sum_scale(int bias) { return bias > 6 ? 1.f / (1 << (bias - 6)) : 1.f; }
+// What turns sums of weights times codes, over the weights' sum, into outputs.
+constexpr float out_scale(int bias) { return sum_scale(bias) / 127.f; }
+// The log-sum-exp of a row from its reference and sum.
+__device__ __forceinline__ float row_lse(float m, float sum, int bias) {
+  return (m + (float)(bias - 6) + log2f(sum)) * 0.69314718056f;
+}
+
 // Two 8-bit codes of a word whose sign bits are flipped (u = q + 128), as halves: 0x6400 + u is
 // the half 1024 + u, and subtracting 1152 leaves q, both exact.
 __device__ __forceinline__ uint32_t codes_f16(uint32_t u, uint32_t pick) {

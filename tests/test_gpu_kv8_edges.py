@@ -45,3 +45,62 @@ def test_bad_pages_stay_with_the_rows_that_see_them(torch, D, new, side, bad):
     _close(got[~sees], want[~sees], tol[~sees], "rows that see only finite pages")
     _close(got_lse[~sees], lse[~sees], ltol[~sees], "their lse")
     assert np.isnan(got[sees]).all()
+
+
+# --------------------------------------------------------------------------- weights far below the largest
+
+def one_key_draws(torch, keys, new, copies, D, dtype, at, gap, group=4, page=64, size=1.0, rest=None):
+    """`copies` sequences that share their pages and queries, so that one block goes through many keys.  Key
+    `at` has a score `gap` (and up to a quarter more, head by head) above all others, which tie.  Its own value
+    is small and of both signs; the others' are positive.  `rest`: the value magnitude of pages other than
+    that of `at`, where it is not `size`."""
+    pages = -(-keys // page)
+    s = Setup(torch, [keys - new], [new], 1, D, page, dtype, seed=keys + D, total=pages + 2)
+    shape = (pages + 2, 1, page, D)
+    s.codes = {x: s.rs.randint(-127, 128, shape).astype(np.int8) for x in "kv"}
+    s.codes["v"] = np.abs(s.codes["v"])
+    s.amax = {"k": np.ones(shape[:2]), "v": np.full(shape[:2], float(s.rounded(size if rest is None else rest)))}
+    own = s.table[0, at // page]
+    s.amax["v"][own] = float(s.rounded(size))
+    s.codes["k"][:, :, :, 0] = 0
+    s.codes["k"][own, 0, at % page, 0] = 127
+    s.codes["v"][own, 0, at % page] = s.rs.randint(-5, 6, D)
+    s.table, s.len, s.new = s.table.repeat(copies, 0), s.len.repeat(copies), s.new.repeat(copies)
+    s.T, s.q_start = new * copies, new * np.arange(copies + 1)
+    q = s.rows(group) * 0
+    q[:, :, 0] = torch.linspace(1.0, 1.25, group).to(s.dt)
+    return s.upload(), q
+
+
+def check_small_weights(torch, s, q, scale, floor, step):
+    """As check_attention, for weights that are off by `floor` of the largest weight-times-magnitude where that
+    is more than 2^-11 of their own, and sums that take `step` keys at a time: fp32 additions, 2^-25 (the
+    products' may drop bits: 2^-23) of the total each."""
+    n, new, heads = int(s.len[0]), int(s.new[0]), q.shape[1]
+    out = torch.empty((s.T, heads, s.D), dtype=s.dt, device="cuda")
+    lse = torch.empty((s.T, heads), device="cuda")
+    ws = q4.new_workspace(q4.lily_kv8_attention_workspace_bytes(s.cache, s.batch, s.T, heads))
+    q4.lily_kv8_attention(s.cache, s.batch, q.cuda(), out, scale, lse=lse, ws=ws)
+    assert q4.lily_q4_workspace_status(ws) == q4.OK
+    k, v = (plain.values(s.codes[x], s.amax[x], s.table[0], n) for x in "kv")
+    mag = np.repeat(s.amax["v"][s.table[0][:-(-n // s.page)]].T, s.page, 1)[:, :n]
+    o, l, size, top, reach = plain.attention(_f64(q[:new]), k, v, mag, scale, True, 0)
+    d, sums = 2.0 ** -21 * reach, n / step * 2.0 ** -25
+    tol = (torch.finfo(s.dt).eps / 2 * np.abs(o) + (2.0 ** -11 + 2.0 ** -18 + 5 * sums + 2 * d[..., None]) * size
+           + n * floor * top[..., None] + torch.finfo(s.dt).smallest_normal * torch.finfo(s.dt).eps / 2)
+    copies = len(s.len)
+    for b in {0, copies // 2, copies - 1}:
+        _close(_f64(out[b * new:(b + 1) * new]), o, tol, "out")
+        _close(_f64(lse[b * new:(b + 1) * new]), l, d + 2.0 ** -18 + sums + 2.0 ** -22 * np.abs(l), "lse")
+
+
+@pytest.mark.parametrize("keys,copies,D,dtype,at,gap", [
+    (33000, 300, 128, "bfloat16", 5, 17.5), (40000, 200, 256, "bfloat16", 39999, 17.5), (30000, 400, 64, "float16", 15000, 17.0),
+    (1000, 1, 64, "float16", 500, 13.0), (262144, 1, 256, "bfloat16", 0, 17.5),
+])
+def test_small_weights_count(torch, keys, copies, D, dtype, at, gap):
+    """One key draws most of the weight and carries little; what all others add is about 2^-25 of it
+    each.  Weights are at most 2^14 in fp16, whose last step is 2^-24: half of it is 2^-39 of the largest.
+    A block's four warps take 16 keys at a time each."""
+    s, q = one_key_draws(torch, keys, 1, copies, D, dtype, at, gap)
+    check_small_weights(torch, s, q, gap, 2.0 ** -39, 64)
