@@ -24,11 +24,12 @@
 // q after a scaling by a power of two; the weights are rounded to fp16 relative to the largest
 // weight-times-magnitude (see kv8_attention.cu for the magnitudes' place in the exponent).
 //
-// The running maximum moves only when a row's grows by more than 2^8 (weights up to 256 are as exact
-// in fp16), because moving it rescales O in tensor memory.  Head_dim 64 and 128 need no maximum before
-// the weights then: a tile is done in one pass to the maximum there is, and done again where a row's
-// weights come to more than 2^15 (ragged prompts below: 657 us with a pass for the maximum, 608 with
-// the maximum beside the weights, 583 with their sum, which is there anyway, as the sign).  The pass
+// A row's reference m is set 6 below the largest exponent there is (see kv8_device.cuh) and moves only when
+// one grows to 15 above it (head_dim 64 and 128: to 11.9), where fp16 still holds its weight, because
+// moving it rescales O in tensor memory.  Head_dim 64 and 128 need no maximum before
+// the weights then: a tile is done in one pass to the reference there is, and done again where sixteen of a
+// row's weights come to more than 65504 (ragged prompts below: 657 us with a pass for the maximum, 608 with
+// the maximum beside the weights, 583 with their sums, which are there anyway, as the sign).  The pass
 // holds a row's 64 words of weights until it is known to stand, so the softmax warps take registers
 // from the issuing warp's group (160 a thread and 64; 168 and 40: 586 us; 152 and 80: 620 us; 144 and
 // 96: 609 us).  Head_dim 256 has no registers for it.
@@ -50,6 +51,10 @@
 namespace lq4 {
 
 constexpr int kRows = 128, kKeys = 128;
+// A row's reference below the largest exponent when it is set.  More of it keeps smaller weights, less leaves
+// more room before the reference has to move: 5 x 1500 prompts over 3000 keys, heads of 128, 460 us at 0 and 5,
+// 462 at 6, 469 at 7; with scores four times as spread 631, 655, 658, 661.
+constexpr int kBias = 6;
 
 template <int D>
 struct PromptShape {
@@ -63,6 +68,9 @@ struct PromptShape {
   static constexpr int TILE = kKeys * D * 2;    // bytes of a K or V tile (and of 128 rows of Q)
   static constexpr int VW = D == 64 ? 2 : 4;    // words of a token a lane holds of V
   static constexpr int COLS = D == 256 ? 16 : 32;  // score columns a thread holds, twice
+  // The exponent above a row's reference beyond which it moves.  fp16 holds weights below 2^16; sixteen whose
+  // sum is above 65504 have one above 2^11.9, so that the one pass never finds too much and moves nothing.
+  static constexpr float MOVE = D == 256 ? 15.f : 11.9f;
   static constexpr int SMEM = (NQ + 2 * KB) * TILE + 1024;
 };
 
@@ -379,7 +387,7 @@ __global__ void __launch_bounds__(PromptShape<D>::THREADS, 1)
       const bool whole = !__any_sync(~0u, page < 0) && k0 >= all_lo && k0 + kKeys <= all_hi;
       // the reciprocal is a number for a magnitude of NaN too: a hidden key's weight of 0 times it is 0, and
       // the rows that see the page have its NaN from the logarithm
-      if (lane < 8) meta[lane] = make_float4(page < 0 ? -1.f : mag.x, __log2f(va), fminf(__frcp_rn(va), 2e30f), 0.f);
+      if (lane < 8) meta[lane] = make_float4(page < 0 ? -1.f : mag.x, __log2f(va), fminf(__frcp_rn(va), 2e30f) * sum_scale(kBias), 0.f);
       page = check_page(B, raw, a.hdr);
       mag = load_mag(page);
       raw = page_of(j + 2 * STEP, lane & 7);
@@ -434,18 +442,17 @@ __global__ void __launch_bounds__(PromptShape<D>::THREADS, 1)
         return both.x + both.y;
       };
       if (NQ == 2 && whole && j > 0) {
-        // One pass: the weights to the running maximum as it is, in registers.  Weights up to 2^15 are
-        // as exact in fp16 as those below 1, and none is more than their sum; only where a row's sum is
-        // more, or the row has no maximum yet, does the warp do the tile again (its scores are still
-        // there).  128 weights that come to more than 2^15 have one above 2^8: the maximum moves then.
+        // One pass: the weights to the reference as it is, in registers.  No weight is more than the sum of
+        // its group; only where a row has one above 65504, or has no reference yet, does the warp do
+        // the tile again (its scores are still there).
         const float m0 = m == -INFINITY ? 0.f : m;
         uint32_t p[64];
-        float sum = l, all = 0.f;
+        float sum = 0.f, most = 0.f;
         for_columns<16, 4>(t_s, [&](int c, const uint32_t *s) {
-          all += group_weights(s, meta[c], m0, p + 8 * c, sum);
+          most = fmaxf(most, group_weights(s, meta[c], m0, p + 8 * c, sum));
         });
-        if (!__any_sync(~0u, all > 32768.f || m == -INFINITY)) {
-          l = sum;
+        if (!__any_sync(~0u, most > 65504.f || m == -INFINITY)) {
+          l += sum;
 #pragma unroll
           for (int i = 0; i < 64; i += 8) tm_st8(t_s + i, p + i);
           tm_st_wait();
@@ -460,7 +467,7 @@ __global__ void __launch_bounds__(PromptShape<D>::THREADS, 1)
         for (int g = 0; g < P::COLS / 16; ++g)
           group_top(s + 16 * g, meta[c * (P::COLS / 16) + g], top);
       });
-      // move the running maximum?  (the first tile sets it: O is not there yet)
+      // move the reference?  (the first tile sets it: O is not there yet)
       if (NQ == 1) {  // the other group's last tile has decided
         if (j > 0) {
           if (!(ok = wait_warp(m_full + 8 * (wg ^ 1), ((j - 1) >> 1) & 1, abort_flag, err))) break;
@@ -471,9 +478,9 @@ __global__ void __launch_bounds__(PromptShape<D>::THREADS, 1)
           }
         }
       }
-      const bool move = top > m + 8.f || (m == -INFINITY && top > m);
+      const bool move = top > m + P::MOVE || (m == -INFINITY && top > m);
       if (__any_sync(~0u, move)) {
-        const float now = move ? top : m;
+        const float now = move ? top - (float)kBias : m;
         const float f = move ? ex2_approx(m - now) : 1.f;
         m = now;
         l *= f;
@@ -543,7 +550,7 @@ __global__ void __launch_bounds__(PromptShape<D>::THREADS, 1)
         }
         if (first) a.ml[at] = make_float2(none ? -INFINITY : m, none ? 0.f : l);
       } else {
-        const float f = none ? 0.f : 1.f / (127.f * l);
+        const float f = none ? 0.f : out_scale(kBias) / l;
         uint4 *dst = reinterpret_cast<uint4 *>(a.out + row * a.o_ts + (int64_t)head * a.o_hs);
 #pragma unroll 1
         for (int c = c0; c < c1; ++c) {
@@ -559,7 +566,7 @@ __global__ void __launch_bounds__(PromptShape<D>::THREADS, 1)
         }
         if (a.lse && live && first)
           a.lse[row * a.kv_heads * a.group + head] =
-              none ? -INFINITY : (m + log2f(l)) * 0.69314718056f;
+              none ? -INFINITY : row_lse(m, l, kBias);
       }
     }
     tc::tc_fence_before();
@@ -864,7 +871,9 @@ __global__ void __launch_bounds__(256) kv8_prompt_join_kernel(AttnArgs a, int bf
       acc[2 * i + 1] = fmaf(u.y, f, acc[2 * i + 1]);
     }
   }
-  const float f = top == -INFINITY ? 0.f : 1.f / (127.f * den);
+  const float f = top == -INFINITY ? 0.f : 1.f / den;
+#pragma unroll
+  for (int i = 0; i < E; ++i) acc[i] *= out_scale(kBias);
   uint32_t *dst = reinterpret_cast<uint32_t *>(a.out + row * a.o_ts + (int64_t)head * a.o_hs) + lane;
 #pragma unroll
   for (int i = 0; i < E / 2; ++i)
@@ -872,7 +881,7 @@ __global__ void __launch_bounds__(256) kv8_prompt_join_kernel(AttnArgs a, int bf
                        : F16::from_f32x2(acc[2 * i] * f, acc[2 * i + 1] * f);
   if (a.lse && lane == 0)
     a.lse[row * a.kv_heads * a.group + head] =
-        top == -INFINITY ? -INFINITY : (top + log2f(den)) * 0.69314718056f;
+        top == -INFINITY ? -INFINITY : row_lse(top, den, kBias);
 }
 
 // ----------------------------------------------------------------------------- launches

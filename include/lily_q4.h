@@ -411,7 +411,8 @@ LILY_Q4_API int lily_kv8_read(const lily_kv8_cache *cache, const lily_kv8_batch 
  * lse: fp32 [T][q_heads] or NULL.  Scores, statistics and sums are fp32; the products take the
  * codes exactly (fp16 holds them) against q scaled to fp16 by a power of two for each row (exact
  * for elements down to 2^-28 of the row's largest), and the softmax weights, times their
- * page's value magnitude over the running maximum of that product, in fp16.
+ * page's value magnitude over the largest such product, in fp16: relative to 2^-11 down to 2^-28 of the
+ * largest (prompt chunks: 2^-20), absolute to 2^-39 (2^-31) of it below.
  * Values below 1e-32 in magnitude count as that small, not as what they are.
  * q_heads: a multiple of kv_heads, at most 128 a key/value head.
  */

@@ -104,3 +104,14 @@ def test_small_weights_count(torch, keys, copies, D, dtype, at, gap):
     A block's four warps take 16 keys at a time each."""
     s, q = one_key_draws(torch, keys, 1, copies, D, dtype, at, gap)
     check_small_weights(torch, s, q, gap, 2.0 ** -39, 64)
+
+
+@pytest.mark.parametrize("keys,copies,D,dtype,at,gap", [
+    (65536, 160, 128, "float16", 0, 17.5), (65536, 160, 256, "bfloat16", 30000, 17.5), (33000, 160, 64, "float16", 32900, 17.0),
+    (131072, 1, 256, "float16", 65536, 17.5),
+])
+def test_small_weights_count_in_prompts(torch, keys, copies, D, dtype, at, gap):
+    """The same for prompts of 40 tokens: the first maximum is at weight 2^6, so the fp16 weights' last half step
+    is 2^-31 of the largest at most.  Products take 16 keys at a time."""
+    s, q = one_key_draws(torch, keys, 40, copies, D, dtype, at, gap)
+    check_small_weights(torch, s, q, gap, 2.0 ** -31, 16)
