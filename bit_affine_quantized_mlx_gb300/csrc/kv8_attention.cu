@@ -370,8 +370,7 @@ __global__ void __launch_bounds__(kDecThreads, decode_blocks(D, NT)) kv8_decode_
           }
         }
         const float ka = mt[j];
-        float va = mt[NG + j];
-        va = va < 1e-30f ? 1e-30f : va;
+        const float va = value_size(mt[NG + j]);
         iv[j] = fminf(__frcp_rn(va), 2e30f) * sum_scale(kBias);  // a number for a magnitude of NaN too: 0 times it is 0
         const float lv = __log2f(va);
         const int tk = tok0 + 16 * j;
@@ -405,9 +404,10 @@ __global__ void __launch_bounds__(kDecThreads, decode_blocks(D, NT)) kv8_decode_
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const float now = fmaxf(m[n][e], top[n][e]);
-            const float f = now == -INFINITY ? 1.f : ex2(m[n][e] - now);
+            const Moved by(m[n][e], now == -INFINITY ? m[n][e] : now);
+            const float f = now == -INFINITY ? 1.f : by.factor();
+            l[n][e] = now == -INFINITY ? l[n][e] : by.sum(l[n][e]);
             m[n][e] = now;
-            l[n][e] *= f;
 #pragma unroll
             for (int k = 0; k < MT; ++k) {
               o[k][n][e] *= f;
@@ -488,7 +488,7 @@ __global__ void __launch_bounds__(kDecThreads, decode_blocks(D, NT)) kv8_decode_
       for (int w = 0; w < kDecWarps; ++w) {
         const float mw = s_m[w * RT + tid];
         // without a maximum the sum is 0, or NaN for a row of NaN
-        den += s_l[w * RT + tid] * (mw == -INFINITY ? 1.f : ex2(mw - top));
+        den += mw == -INFINITY ? s_l[w * RT + tid] : Moved(mw, top).sum(s_l[w * RT + tid]);
       }
       s_fin[tid] = make_float2(top, den);
       s_qf[tid] = den == 0.f ? 0.f : 1.f / den;  // q's factors are not needed any more
@@ -620,9 +620,10 @@ __global__ void __launch_bounds__(kJoinThreads) kv8_join_kernel(AttnArgs a, int 
   float den = 0.f;
 #pragma unroll
   for (int k = 0; k < MINE; ++k) {
-    const float f = ml[k].x == -INFINITY ? 1.f : ex2(ml[k].x - top);  // sum and output 0, or NaN
-    s_w[tid + k * kJoinThreads] = f;
-    den = fmaf(f, ml[k].y, den);
+    const bool none = ml[k].x == -INFINITY;  // sum and output 0, or NaN
+    const Moved by(none ? 0.f : ml[k].x, none ? 0.f : top);
+    s_w[tid + k * kJoinThreads] = by.factor();
+    den += by.sum(ml[k].y);
   }
 #pragma unroll
   for (int o = 16; o; o >>= 1) den += __shfl_xor_sync(~0u, den, o);

@@ -164,6 +164,23 @@ __device__ __forceinline__ float row_lse(float m, float sum, int bias) {
   return (m + (float)(bias - 6) + log2f(sum)) * 0.69314718056f;
 }
 
+// The magnitude that a page's values count with in the exponents.  What a page of zeros counts with does
+// not matter to the output, but its weights have to stay in the sum: 2^(x - m) is 0 below 2^-126, so beside
+// values of 6e4 all weights below 2^-24 of the largest were lost with 1e-30.  With 2^-80 they are there down
+// to 2^-36 (prompt chunks; 2^-44 else), and values down to 1e-30 beside such a page still have full weights.
+__device__ __forceinline__ float value_size(float a) {
+  return a < 1e-30f ? (a == 0.f ? 0x1p-80f : 1e-30f) : a;
+}
+
+// A row's sum moved from reference m to now (not below it): half of the way twice, because the sum of
+// pages that count as small can be as large as 2^(m - now) is small.
+struct Moved {
+  float half;
+  __device__ __forceinline__ Moved(float m, float now) { asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(half) : "f"(0.5f * (m - now))); }
+  __device__ __forceinline__ float factor() const { return half * half; }
+  __device__ __forceinline__ float sum(float l) const { return l * half * half; }
+};
+
 // Two 8-bit codes of a word whose sign bits are flipped (u = q + 128), as halves: 0x6400 + u is
 // the half 1024 + u, and subtracting 1152 leaves q, both exact.
 __device__ __forceinline__ uint32_t codes_f16(uint32_t u, uint32_t pick) {

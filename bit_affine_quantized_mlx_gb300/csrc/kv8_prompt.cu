@@ -383,7 +383,7 @@ __global__ void __launch_bounds__(PromptShape<D>::THREADS, 1)
     for (int j = j_first; j < j_end; j += STEP) {
       const int k0 = key0 + j * kKeys;
       const uint32_t turn = (NQ == 2 ? j : j >> 1) & 1;
-      const float va = page < 0 ? 1.f : mag.y < 1e-30f ? 1e-30f : mag.y;
+      const float va = page < 0 ? 1.f : value_size(mag.y);
       const bool whole = !__any_sync(~0u, page < 0) && k0 >= all_lo && k0 + kKeys <= all_hi;
       // the reciprocal is a number for a magnitude of NaN too: a hidden key's weight of 0 times it is 0, and
       // the rows that see the page have its NaN from the logarithm
@@ -473,7 +473,7 @@ __global__ void __launch_bounds__(PromptShape<D>::THREADS, 1)
           if (!(ok = wait_warp(m_full + 8 * (wg ^ 1), ((j - 1) >> 1) & 1, abort_flag, err))) break;
           const float held = s_max[r];
           if (held != m) {
-            l *= m == -INFINITY ? 0.f : ex2_approx(m - held);
+            l = m == -INFINITY ? 0.f : Moved(m, held).sum(l);
             m = held;
           }
         }
@@ -481,9 +481,10 @@ __global__ void __launch_bounds__(PromptShape<D>::THREADS, 1)
       const bool move = top > m + P::MOVE || (m == -INFINITY && top > m);
       if (__any_sync(~0u, move)) {
         const float now = move ? top - (float)kBias : m;
-        const float f = move ? ex2_approx(m - now) : 1.f;
+        const Moved by(move ? m : 0.f, move ? now : 0.f);
+        const float f = by.factor();
+        l = by.sum(l);
         m = now;
-        l *= f;
         if (NQ == 1) s_max[r] = m;
         if (j > 0) {
           // O is only touched between the product of the last tile and that of this one
@@ -524,7 +525,7 @@ __global__ void __launch_bounds__(PromptShape<D>::THREADS, 1)
       asm volatile("bar.sync 2, 256;" ::: "memory");
       const float2 x = s_ml[0][r], y = s_ml[1][r];
       m = fmaxf(x.x, y.x);
-      l = x.y * (x.x == -INFINITY ? 1.f : ex2_approx(x.x - m)) + y.y * (y.x == -INFINITY ? 1.f : ex2_approx(y.x - m));
+      l = (x.x == -INFINITY ? x.y : Moved(x.x, m).sum(x.y)) + (y.x == -INFINITY ? y.y : Moved(y.x, m).sum(y.y));
     }
     if (ok && j_end > 0) ok = wait_pv(j_end - 1);
     tc::tc_fence_after();
@@ -861,8 +862,9 @@ __global__ void __launch_bounds__(256) kv8_prompt_join_kernel(AttnArgs a, int bf
     const int64_t at = ((int64_t)item * splits + s) * ROWS + r;
     const float2 ml = a.ml[at];
     if (ml.x == -INFINITY) continue;  // its output was not written
-    const float f = ex2_approx(ml.x - top);
-    den = fmaf(ml.y, f, den);
+    const Moved by(ml.x, top);
+    const float f = by.factor();
+    den += by.sum(ml.y);
     const float2 *src = reinterpret_cast<const float2 *>(a.part + at * D) + lane;
 #pragma unroll
     for (int i = 0; i < E / 2; ++i) {

@@ -413,7 +413,7 @@ LILY_Q4_API int lily_kv8_read(const lily_kv8_cache *cache, const lily_kv8_batch 
  * for elements down to 2^-28 of the row's largest), and the softmax weights, times their
  * page's value magnitude over the largest such product, in fp16: relative to 2^-11 down to 2^-28 of the
  * largest (prompt chunks: 2^-20), absolute to 2^-39 (2^-31) of it below.
- * Values below 1e-32 in magnitude count as that small, not as what they are.
+ * Pages whose values' magnitude is below 1e-30, but not 0, count as of that magnitude.
  * q_heads: a multiple of kv_heads, at most 128 a key/value head.
  */
 LILY_Q4_API int lily_kv8_attention(const lily_kv8_cache *cache, const lily_kv8_batch *batch,

@@ -115,3 +115,24 @@ def test_small_weights_count_in_prompts(torch, keys, copies, D, dtype, at, gap):
     is 2^-31 of the largest at most.  Products take 16 keys at a time."""
     s, q = one_key_draws(torch, keys, 40, copies, D, dtype, at, gap)
     check_small_weights(torch, s, q, gap, 2.0 ** -31, 16)
+
+
+@pytest.mark.parametrize("keys,new,copies,D,at,gap", [
+    (33000, 1, 300, 128, 7, 17.5), (33000, 1, 200, 256, 30000, 17.5), (262144, 1, 1, 128, 7, 18.0), (262144, 1, 1, 256, 100000, 18.0),
+    (65536, 40, 160, 64, 7, 13.5), (65536, 40, 160, 256, 65000, 13.5), (65536, 40, 160, 128, 40000, 13.5), (131072, 40, 1, 128, 7, 13.5),
+])
+def test_zero_values_stay_in_the_sum(torch, keys, new, copies, D, at, gap):
+    """Pages of zero values beside one of values near fp16's largest: they add nothing to the output, but
+    their weights count, in a block's running sum and where parts are joined."""
+    s, q = one_key_draws(torch, keys, new, copies, D, "float16", at, gap, size=6e4, rest=0.0)
+    check_small_weights(torch, s, q, gap, *((2.0 ** -39, 64) if new == 1 else (2.0 ** -31, 16)))
+
+
+@pytest.mark.parametrize("new", [1, 60])
+def test_small_values_beside_zero_ones(torch, new):
+    """Values of 1e-18 keep their bits beside pages of zeros, which count as of 2^-80 (8e-25)."""
+    s = Setup(torch, [400], [new], 1, 128, 16, "bfloat16")
+    own = s.table[0, :-(-int(s.len[0]) // 16)]
+    s.amax["v"][own, 0] = s.rounded(1e-18)
+    s.amax["v"][own[::3], 0] = 0
+    check_attention(torch, s.upload(), 4, 0.1)
