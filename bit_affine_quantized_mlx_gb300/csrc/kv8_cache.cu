@@ -244,8 +244,11 @@ __global__ void __launch_bounds__(kReadThreads) kv8_read_kernel(CacheArgs a) {
       if (at[r] < 0) continue;
       float f[16];
       const uint32_t u[4] = {w[r].x, w[r].y, w[r].z, w[r].w};
+      // q amax passes fp32's range for magnitudes near the top of it: 2^-8 of it, exactly, does not
+      const bool far = s[r] > 0x1p100f;
+      const float size = far ? s[r] * 0x1p-8f : s[r], step = far ? 256.f / 127.f : 1.f / 127.f;
 #pragma unroll
-      for (int e = 0; e < 16; ++e) f[e] = (float)(int8_t)(u[e >> 2] >> (8 * (e & 3))) * s[r] * (1.f / 127.f);
+      for (int e = 0; e < 16; ++e) f[e] = (float)(int8_t)(u[e >> 2] >> (8 * (e & 3))) * size * step;
       if (DT == LILY_F32) {
         float *o = static_cast<float *>(a.y[kv]) + at[r];
 #pragma unroll

@@ -136,3 +136,25 @@ def test_small_values_beside_zero_ones(torch, new):
     s.amax["v"][own, 0] = s.rounded(1e-18)
     s.amax["v"][own[::3], 0] = 0
     check_attention(torch, s.upload(), 4, 0.1)
+
+
+# --------------------------------------------------------------------------- ends of the types' ranges
+
+@pytest.mark.parametrize("top", [1e30, 2.6e36, 2.8e36, 1e37, 3.3e38])
+def test_read_near_the_top_of_the_range(torch, top):
+    """Finite tokens read back finite, to the code's resolution and the output's rounding."""
+    s = Setup(torch, [0], [20], 2, 64, 16, "bfloat16").upload()
+    x = s.rows(2)
+    x = (x.double() / x.double().abs().max() * top).to(s.dt)
+    assert torch.isfinite(x).all()
+    ws = q4.new_workspace(256)
+    q4.lily_kv8_append(s.cache, s.batch, x.cuda(), x.cuda(), ws=ws)
+    plain.append(s.codes["k"], s.amax["k"], s.table, s.q_start, s.len, _f64(x))
+    want = plain.values(s.codes["k"], s.amax["k"], s.table[0], 20).transpose(1, 0, 2)
+    for dt in (torch.float32, torch.bfloat16):
+        k, v = (torch.empty((20, 2, 64), dtype=dt, device="cuda") for _ in "kv")
+        q4.lily_kv8_read(s.cache, s.batch, k, v, ws=ws)
+        # q amax is exact; the reciprocal of 127 and the product with it are rounded; then the output's rounding
+        _close(_f64(k), want, (2.0 ** -23 + torch.finfo(dt).eps / 2) * np.abs(want), str(dt))
+        assert torch.equal(k, v)
+    assert q4.lily_q4_workspace_status(ws) == q4.OK
