@@ -158,3 +158,14 @@ def test_read_near_the_top_of_the_range(torch, top):
         _close(_f64(k), want, (2.0 ** -23 + torch.finfo(dt).eps / 2) * np.abs(want), str(dt))
         assert torch.equal(k, v)
     assert q4.lily_q4_workspace_status(ws) == q4.OK
+
+
+@pytest.mark.parametrize("new", [1, 50])
+def test_queries_near_the_top_of_the_range(torch, new):
+    """Queries up to 3e38 with scores of ordinary size (a scale as small as they are large)."""
+    s = Setup(torch, [100], [new], 1, 64, 32, "bfloat16").upload()
+    q = s.rows(8).double()
+    q /= q.abs().amax(-1, keepdim=True)
+    q = (q * torch.tensor([1e28, 1e30, 3e30, 1e31, 1e33, 1e36, 1e38, 3.3e38], dtype=torch.float64)[:, None]).to(s.dt)
+    assert torch.isfinite(q).all()
+    check_attention(torch, s, 8, 2e-36, q=q)
