@@ -131,7 +131,7 @@ __global__ void __launch_bounds__(kDecThreads, decode_blocks(D, NT)) kv8_decode_
 
   // key range of a sequence (the union of its rows' ranges) and its number of tiles
   auto range_of = [&](const Seq &s, int &lo, int &nt) {
-    lo = a.window ? max(0, s.len - s.n - a.window + 1) & ~15 : 0;
+    lo = max(0, first_key(s.len - s.n, a.window)) & ~15;
     nt = max(1, (s.len - lo + TILE - 1) / TILE);
   };
   int base_count = 0;
@@ -273,7 +273,7 @@ __global__ void __launch_bounds__(kDecThreads, decode_blocks(D, NT)) kv8_decode_
       }
 #pragma unroll
       for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
-      const int e = top > 0.f ? min(max(ilogbf(top), -100), 100) : 14;
+      const int e = top > 0.f ? min(max(ilogbf(top), -100), 127) : 14;
       const float up = __uint_as_float((uint32_t)(127 + 14 - e) << 23);
 #pragma unroll
       for (int i = 0; i < E / 2; ++i)
@@ -304,13 +304,13 @@ __global__ void __launch_bounds__(kDecThreads, decode_blocks(D, NT)) kv8_decode_
       for (int e = 0; e < 2; ++e) {
         const int r = n * 8 + 2 * t + e, p = sq.len - sq.n + (rt * RT + r) / a.group;
         qf[n][e] = s_qf[r];
-        klo[n][e] = a.window ? p - a.window + 1 : 0;
+        klo[n][e] = first_key(p, a.window);
         khi[n][e] = a.causal ? min(p + 1, sq.len) : sq.len;
       }
     // keys that every row of the tile sees
     const int p_first = sq.len - sq.n + rt * RT / a.group;
     const int p_last = sq.len - sq.n + min(sq.n - 1, (rt * RT + RT - 1) / a.group);
-    const int all_lo = a.window ? p_last - a.window + 1 : 0;
+    const int all_lo = first_key(p_last, a.window);
     const int all_hi = a.causal ? min(p_first + 1, sq.len) : sq.len;
 
     float m[NT][2], l[NT][2], o[MT][NT][4];

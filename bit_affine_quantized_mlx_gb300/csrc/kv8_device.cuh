@@ -112,6 +112,10 @@ __device__ __forceinline__ int find_seq(const Batch &B, int t) {
   return lo;
 }
 
+// The first key (or one before key 0) that a row at position p sees in a window, 0 for none.  Positions before
+// the first, where there are more rows than tokens, are cut off: less a window near 2^31 they would wrap.
+__device__ __forceinline__ int first_key(int p, int window) { return window ? max(p, 0) - window + 1 : 0; }
+
 // Page number of entry i of sequence b, as it stands: checked where it is used (check_page), so that
 // a load ahead of its use does not have to be waited for.
 __device__ __forceinline__ int raw_page(const Batch &B, int b, int i) {

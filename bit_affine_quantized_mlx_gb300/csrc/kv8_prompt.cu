@@ -284,7 +284,7 @@ __global__ void __launch_bounds__(PromptShape<D>::THREADS, 1)
     it.rt = s_found[1];
     const int p_first = s.len - s.n + it.rt * P::ROWS / a.group;
     const int p_last = s.len - s.n + min(s.n - 1, (it.rt * P::ROWS + P::ROWS - 1) / a.group);
-    it.lo = a.window ? max(0, p_first - a.window + 1) & ~15 : 0;
+    it.lo = max(0, first_key(p_first, a.window)) & ~15;
     const int hi = a.causal ? min(p_last + 1, s.len) : s.len;
     it.tiles = max(0, (hi - it.lo + kKeys - 1) / kKeys);
   }
@@ -336,7 +336,7 @@ __global__ void __launch_bounds__(PromptShape<D>::THREADS, 1)
         asm volatile("bar.sync 2, 256;" ::: "memory");
         top = fmaxf(top, s_ml[wg ^ 1][r].x);
       }
-      const int e = top > 0.f ? min(max(ilogbf(top), -100), 100) : 14;
+      const int e = top > 0.f ? min(max(ilogbf(top), -100), 127) : 14;
       const float up = copysignf(__uint_as_float((uint32_t)(127 + 14 - e) << 23), a.scale2);
       qf = __uint_as_float((uint32_t)(127 - 14 + e) << 23) * fabsf(a.scale2);
       uint8_t *dst = mem + (NQ == 2 ? wg * P::TILE : 0);
@@ -354,7 +354,7 @@ __global__ void __launch_bounds__(PromptShape<D>::THREADS, 1)
     asm volatile("bar.sync 1, 288;" ::: "memory");  // q is there: softmax and issuing warps
     // visible keys of this row, and those that every live row of the warp sees
     const int pos = it.len - it.n + tok;
-    const int klo = a.window ? pos - a.window + 1 : 0, khi = a.causal ? min(pos + 1, len) : len;
+    const int klo = first_key(pos, a.window), khi = a.causal ? min(pos + 1, len) : len;
     const int all_lo = __reduce_max_sync(~0u, live ? klo : INT_MIN);
     const int all_hi = __reduce_min_sync(~0u, live ? khi : INT_MAX);
     const uint32_t t_row = tmem + ((uint32_t)((warp & 3) * 32) << 16);

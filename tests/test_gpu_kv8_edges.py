@@ -169,3 +169,14 @@ def test_queries_near_the_top_of_the_range(torch, new):
     q = (q * torch.tensor([1e28, 1e30, 3e30, 1e31, 1e33, 1e36, 1e38, 3.3e38], dtype=torch.float64)[:, None]).to(s.dt)
     assert torch.isfinite(q).all()
     check_attention(torch, s, 8, 2e-36, q=q)
+
+
+# --------------------------------------------------------------------------- positions and windows near 2^31
+
+@pytest.mark.parametrize("window", [(1 << 31) - 1, (1 << 31) - 4, 1 << 30, 300])
+@pytest.mark.parametrize("new,causal", [(8, False), (8, True), (70, False), (70, True)])
+def test_widest_windows_and_rows_before_the_first_position(torch, new, causal, window):
+    """Rows at negative positions (more of them than tokens) in a window as wide as its type takes: position
+    less window stays in range."""
+    s = Setup(torch, [3 - new, 60], [new, new], 2, 64, 16, "bfloat16").upload()
+    check_attention(torch, s, 8, 0.2, causal, window)
