@@ -87,7 +87,7 @@ __global__ void __launch_bounds__(TEAM *TEAMS) kv8_append_kernel(CacheArgs a) {
       continue;
     }
     const int pos = s.len - s.n + (t - s.row0);
-    if (pos < 0 || pos >= B.table_pages * B.page) {
+    if (pos < 0) {  // kv_len is within the table
       record_index_error(a.hdr);
       ++t;
       continue;
@@ -200,7 +200,7 @@ __global__ void __launch_bounds__(kReadThreads) kv8_read_kernel(CacheArgs a) {
     const Seq s = load_seq(B, b, a.hdr);
     const int pos = s.len - s.n + (t - s.row0);
     if (t >= s.row0 && t < s.row0 + s.n) {
-      if (pos < 0 || pos >= B.table_pages * B.page) {
+      if (pos < 0) {  // kv_len is within the table
         record_index_error(a.hdr);
       } else {
         page = check_page(B, raw_page(B, b, pos >> B.page_shift), a.hdr);
@@ -279,7 +279,8 @@ Batch make_batch(const lily_kv8_cache &C, const lily_kv8_batch &b, int T) {
   B.table_pages = b.table_pages;
   B.batch = b.batch;
   B.max_q = b.max_q;
-  B.max_kv = (int)std::min<int64_t>(b.max_kv, (int64_t)b.table_pages * C.page);
+  // Below 2^31 by more than the keys that are looked up ahead of a sequence's end (64 turns of 256).
+  B.max_kv = (int)std::min<int64_t>(std::min(b.max_kv, INT32_MAX - 65535), (int64_t)b.table_pages * C.page);
   B.T = T;
   B.page = C.page;
   while ((1 << B.page_shift) < C.page) ++B.page_shift;

@@ -360,7 +360,7 @@ typedef struct {
  * sequence's last page are not read.  max_q and max_kv are the host's upper bounds of n_b and
  * kv_len[b]; they size the launch.
  * A sequence whose row range or length is out of bounds (n_b > max_q, kv_len > max_kv or more
- * than table_pages pages, rows beyond T) is skipped and a page number outside the cache is
+ * than table_pages pages, rows beyond T; above 2^31 - 65536 in any case) is skipped and a page number outside the cache is
  * passed over (its tokens are not written, read as zero, and masked in attention); either is
  * recorded for lily_q4_workspace_status as LILY_Q4_ERR_INDEX. */
 typedef struct {

@@ -180,3 +180,25 @@ def test_widest_windows_and_rows_before_the_first_position(torch, new, causal, w
     less window stays in range."""
     s = Setup(torch, [3 - new, 60], [new, new], 2, 64, 16, "bfloat16").upload()
     check_attention(torch, s, 8, 0.2, causal, window)
+
+
+@pytest.mark.parametrize("new", [1, 40])
+def test_tables_wider_than_positions(torch, new):
+    """A block table whose pages' tokens pass 2^31, of which few are used."""
+    s = Setup(torch, [30], [new], 1, 64, 128, "bfloat16").upload()
+    wide = torch.full((1, 1 << 24), -9, dtype=torch.int32, device="cuda")
+    used = -(-int(s.len[0]) // 128)
+    wide[0, :used] = s.batch.block_table[0, :used]
+    s.batch = q4.KV8Batch(wide, s.batch.q_start, s.batch.kv_len, new, (1 << 31) - 1)
+    x = s.rows(1)
+    ws = q4.new_workspace(256)
+    q4.lily_kv8_append(s.cache, s.batch, x.cuda(), x.cuda(), ws=ws)
+    k, v = (torch.empty((new, 1, 64), dtype=torch.float32, device="cuda") for _ in "kv")
+    q4.lily_kv8_read(s.cache, s.batch, k, v, ws=ws)
+    assert q4.lily_q4_workspace_status(ws) == q4.OK
+    for y in "kv":
+        plain.append(s.codes[y], s.amax[y], s.table, s.q_start, s.len, _f64(x))
+    for y, got in (("k", k), ("v", v)):
+        want = plain.values(s.codes[y], s.amax[y], s.table[0], int(s.len[0])).transpose(1, 0, 2)[-new:]
+        _close(_f64(got), want, 2.0 ** -22 * np.abs(want), y)
+    check_attention(torch, s, 4, 0.1)
