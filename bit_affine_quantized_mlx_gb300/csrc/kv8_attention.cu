@@ -683,9 +683,11 @@ static DecodePlan decode_plan(const lily_kv8_cache &C, const lily_kv8_batch &b, 
   p.nt = rows <= 8 ? 1 : rows <= 16 || D == 256 ? 2 : 4;
   const int RT = 8 * p.nt, tile = kTurnBytes / D * kDecWarps;
   const int sms = sm_count() > 0 ? sm_count() : 152;
-  const int64_t items = std::min<int64_t>(b.batch, T) * ((rows + RT - 1) / RT) * C.kv_heads;
+  const int64_t per_seq = (rows + RT - 1) / RT * C.kv_heads, items = std::min<int64_t>(b.batch, T) * per_seq;
   const int64_t tiles = std::max<int64_t>(1, ((int64_t)b.max_kv + 16 + tile - 1) / tile);
-  if (items > INT32_MAX / (tiles + kStart)) return p;  // total 0: the tiles have to be countable in 31 bits
+  // total 0: the tiles have to be countable in 31 bits, those of all sequences too, because row ranges on the
+  // device that go backwards (which is recorded) can give the same rows to many
+  if (std::max<int64_t>(1, b.batch) * per_seq > INT32_MAX / (tiles + kStart)) return p;
   p.grid = (int)std::max<int64_t>(1, std::min<int64_t>(std::min(decode_blocks(D, p.nt) * sms, kJoinMost), items * (tiles + kStart)));
   // Few items have many parts each: a large block reads a row's parts together (262,144 tokens, 152
   // parts: 12 us with 256 threads, 8 with 512).  Fewer: small blocks start
