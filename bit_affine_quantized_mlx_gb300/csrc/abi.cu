@@ -198,14 +198,14 @@ int lily_q4_workspace_status(void *ws, lily_q4_stream_t stream) {
   if (cudaStreamSynchronize(st) != cudaSuccess) return LILY_Q4_ERR_CUDA;
   if (cudaMemcpy(hdr, ws, sizeof(hdr), cudaMemcpyDeviceToHost) != cudaSuccess)
     return LILY_Q4_ERR_CUDA;
-  int rc = LILY_Q4_OK;
-  for (const int w : {kHdrIndexError, kHdrError}) {
+  // what is reported is cleared; an index error beside a time-out waits for the next call
+  for (const int w : {kHdrError, kHdrIndexError}) {
     if (hdr[w] == 0) continue;
     if (cudaMemset(static_cast<int32_t *>(ws) + w, 0, sizeof(int32_t)) != cudaSuccess)
       return LILY_Q4_ERR_CUDA;
-    rc = w == kHdrError ? LILY_Q4_ERR_TIMEOUT : LILY_Q4_ERR_INDEX;
+    return w == kHdrError ? LILY_Q4_ERR_TIMEOUT : LILY_Q4_ERR_INDEX;
   }
-  return rc;
+  return LILY_Q4_OK;
 }
 
 int lily_q4_selftest_timeout(void *ws, size_t ws_bytes, int32_t which, lily_q4_stream_t stream) {

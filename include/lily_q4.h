@@ -249,10 +249,11 @@ LILY_Q4_API int lily_q4_moe_launches(const lily_q4_moe_layer *layer, int32_t T, 
 /* Zero-fill a workspace on `stream` (asynchronous). */
 LILY_Q4_API int lily_q4_workspace_init(void *ws, size_t ws_bytes, lily_q4_stream_t stream);
 
-/* Synchronises `stream`, then reads and clears the workspace's device-side error
- * word: LILY_Q4_OK, or LILY_Q4_ERR_TIMEOUT if a bounded wait gave up since the
+/* Synchronises `stream`, then reads and clears the workspace's device-side error:
+ * LILY_Q4_OK, or LILY_Q4_ERR_TIMEOUT if a bounded wait gave up since the
  * last check, or LILY_Q4_ERR_INDEX if one of the lily_kv8_* calls met a length or a page
- * number out of range (a time-out is reported before it). */
+ * number out of range.  Only the error that is reported is cleared: with both, a time-out comes
+ * first and the next check reports the other. */
 LILY_Q4_API int lily_q4_workspace_status(void *ws, lily_q4_stream_t stream);
 
 /*

@@ -202,3 +202,16 @@ def test_tables_wider_than_positions(torch, new):
         want = plain.values(s.codes[y], s.amax[y], s.table[0], int(s.len[0])).transpose(1, 0, 2)[-new:]
         _close(_f64(got), want, 2.0 ** -22 * np.abs(want), y)
     check_attention(torch, s, 4, 0.1)
+
+
+# --------------------------------------------------------------------------- status
+
+def test_status_reports_an_index_error_beside_a_time_out(torch):
+    """Both errors in one workspace: each is reported once, the time-out first."""
+    s = Setup(torch, [40], [1], 1, 64, 16, "bfloat16").upload()
+    s.batch.block_table[0, 2] = 1 << 29
+    ko = torch.empty((1, 1, 64), dtype=torch.bfloat16, device="cuda")
+    ws = q4.new_workspace(4096)
+    q4.lily_q4_selftest_timeout(ws, 1)  # a bounded wait on a barrier that nothing completes
+    q4.lily_kv8_read(s.cache, s.batch, ko, ko.clone(), ws=ws)
+    assert [q4.lily_q4_workspace_status(ws) for _ in range(3)] == [q4.ERR_TIMEOUT, q4.ERR_INDEX, q4.OK]
