@@ -430,6 +430,13 @@ def _require(ok, what):
         raise Q4Error(ERR_INVALID_ARG, what)
 
 
+def _count(n, what):
+    """n as an int that fits the C ABI's 32 bits: ctypes would drop the rest in silence."""
+    n = int(n)
+    _require(-(1 << 31) <= n < 1 << 31, f"{what} {n}")
+    return n
+
+
 def _rows(t, rows, heads, dim, what):
     """(pointer, token stride, head stride) of a [rows, heads, dim] tensor with a dense last axis."""
     step = t.stride()
@@ -452,8 +459,9 @@ def lily_rope_turns(rotary_dim: int, base: float = 10000.0, scaling: str = "none
     """The rotation table of lily_qk_norm_rope: uint64 [rotary_dim / 2] fractions of a turn for
     each position step (host only); see include/lily_q4.h.  ``to_device`` uploads it."""
     _require(scaling in ROPE_SCALING, f"lily_rope_turns: scaling {scaling!r}")
-    turns = np.zeros(max(int(rotary_dim), 0) // 2, dtype=np.uint64)
-    _check(load().lily_rope_turns(int(rotary_dim), float(base), ROPE_SCALING[scaling], float(factor),
+    rotary_dim = _count(rotary_dim, "lily_rope_turns: rotary_dim")
+    turns = np.zeros(max(rotary_dim, 0) // 2, dtype=np.uint64)
+    _check(load().lily_rope_turns(rotary_dim, float(base), ROPE_SCALING[scaling], float(factor),
                                   float(original_len), float(slow), float(fast), turns.ctypes.data),
            "lily_rope_turns")
     return turns
@@ -567,8 +575,8 @@ class KV8Batch:
                  "KV8Batch: block_table [batch, pages], q_start [batch + 1], kv_len [batch]")
         self.block_table, self.q_start, self.kv_len = block_table, q_start, kv_len
         self._c = lily_kv8_batch(_int32(block_table, "block_table"), _int32(q_start, "q_start"),
-                                 _int32(kv_len, "kv_len"), int(block_table.shape[1]), n, int(max_q),
-                                 int(max_kv))
+                                 _int32(kv_len, "kv_len"), int(block_table.shape[1]), n,
+                                 _count(max_q, "KV8Batch: max_q"), _count(max_kv, "KV8Batch: max_kv"))
         self._at = C.addressof(self._c)
 
     def c(self):
@@ -602,8 +610,8 @@ def lily_kv8_read(cache: KV8Cache, batch: KV8Batch, k_out, v_out, ws=None, strea
 
 
 def lily_kv8_attention_workspace_bytes(cache: KV8Cache, batch: KV8Batch, T: int, q_heads: int) -> int:
-    return int(load().lily_kv8_attention_workspace_bytes(C.byref(cache._c), C.byref(batch._c), int(T),
-                                                         int(q_heads)))
+    return int(load().lily_kv8_attention_workspace_bytes(
+        C.byref(cache._c), C.byref(batch._c), _count(T, "T"), _count(q_heads, "q_heads")))
 
 
 def lily_kv8_attention(cache: KV8Cache, batch: KV8Batch, q, out, scale, lse=None, causal=True,

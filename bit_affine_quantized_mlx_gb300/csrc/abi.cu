@@ -388,6 +388,10 @@ int lily_q4_call(int32_t which, const void *words) {
   if (!words || which < 0 || which > LILY_CALL_KV8_ATTENTION) return LILY_Q4_ERR_INVALID_ARG;
   int64_t w[18];  // the words may be unaligned
   memcpy(w, words, (which == LILY_CALL_KV8_APPEND || which == LILY_CALL_KV8_READ ? 13 : 18) * sizeof(int64_t));
+  // the words that stand for 32-bit numbers have to be such
+  static const int kInts[4][6] = {{1, 2, 3, 0}, {2, 3, 0}, {2, 3, 0}, {2, 3, 4, 6, 7, 0}};
+  for (const int *i = kInts[which]; *i; ++i)
+    if (w[*i] != (int32_t)w[*i]) return LILY_Q4_ERR_INVALID_ARG;
   auto ptr = [&](int i) { return reinterpret_cast<void *>(w[i]); };
   auto i32 = [&](int i) { return (int32_t)w[i]; };
   auto stream = [&](int i) { return reinterpret_cast<lily_q4_stream_t>(w[i]); };

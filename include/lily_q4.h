@@ -431,8 +431,8 @@ LILY_Q4_API size_t lily_kv8_attention_workspace_bytes(const lily_kv8_cache *cach
 
 /*
  * lily_q4_call -- one of the attention calls with its arguments in an array of 64-bit words, in the
- * order of its own declaration (integers sign-extended, pointers as integers, `scale` as the bits
- * of a double), for foreign-function interfaces whose cost an argument shows in single-token
+ * order of its own declaration (integers sign-extended: one that needs more than its 32 bits is
+ * LILY_Q4_ERR_INVALID_ARG; pointers as integers, `scale` as the bits of a double), for foreign-function interfaces whose cost an argument shows in single-token
  * steps.  The typed calls above are the interface; this one only forwards to them.
  */
 #define LILY_CALL_QK_NORM_ROPE 0 /* 18 words */
