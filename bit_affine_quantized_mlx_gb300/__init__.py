@@ -398,7 +398,9 @@ def lily_q4_unpack(w: np.ndarray, N: int, K: int) -> np.ndarray:
 
 # Filled on the first call (torch is imported lazily); looked up by name, not imported, on later ones.
 _DTYPES = {}      # torch.dtype -> code
+_HALVES = {}      # the 16-bit ones of them
 _raw_stream = None  # device index -> handle of its current stream
+_current = None     # -> the current device's index
 _int32_t = _float32_t = None
 _call = None      # lily_q4_call: one packed argument costs less than a score of them
 _ROPE = struct.Struct("18q").pack
@@ -407,11 +409,13 @@ _ATTENTION = struct.Struct("5qd12q").pack
 
 
 def _first_use():
-    global _raw_stream, _int32_t, _float32_t, _call
+    global _raw_stream, _current, _int32_t, _float32_t, _call
     torch = _torch()
     _call = load().lily_q4_call
     _int32_t, _float32_t = torch.int32, torch.float32
-    _DTYPES.update({torch.bfloat16: BF16, torch.int16: BF16, torch.float16: F16, torch.float32: F32})
+    _HALVES.update({torch.bfloat16: BF16, torch.int16: BF16, torch.float16: F16})
+    _DTYPES.update({**_HALVES, torch.float32: F32})
+    _current = torch._C._cuda_getDevice
     _raw_stream = torch._C._cuda_getCurrentRawStream
 
 
@@ -437,12 +441,15 @@ def _count(n, what):
     return n
 
 
-def _rows(t, rows, heads, dim, what):
-    """(pointer, token stride, head stride) of a [rows, heads, dim] tensor with a dense last axis."""
-    step = t.stride()
-    if t.shape != (rows, heads, dim) or (step[2] != 1 and t.numel()):
-        raise Q4Error(ERR_INVALID_ARG, f"{what}: shape {tuple(t.shape)}, strides {step}")
-    return t.data_ptr(), step[0], step[1]
+def _device_of(what, *tensors):
+    """The index of the one device (-1: the host) that all of these are on."""
+    dev = tensors[0].get_device()
+    _require(all(t.get_device() == dev for t in tensors), f"{what}: tensors on several devices")
+    return dev
+
+
+def _elsewhere(what):
+    raise Q4Error(ERR_INVALID_ARG, f"{what}: every tensor has to be on the current GPU")
 
 
 def _int32(t, what):
@@ -489,6 +496,8 @@ class QKNormRope:
                                self.dtype or 0, int(bool(normalize)), float(eps),
                                float(weight_offset), float(rope_scale), _ptr(q_weight),
                                _ptr(k_weight), _ptr(turns) if rotary_dim else None)
+        held = [t for t in (q_weight, k_weight, turns if rotary_dim else None) if t is not None]
+        self._dev = _device_of("QKNormRope", *held) if held else None  # None: whatever the heads are on
         self._at = C.addressof(self._c)
 
     def c(self, dtype):
@@ -507,20 +516,28 @@ def lily_qk_norm_rope(op: QKNormRope, q, k, pos, q_out, k_out, stream=None):
     if len(shape) != 3:
         raise Q4Error(ERR_INVALID_ARG, f"lily_qk_norm_rope: q {tuple(shape)}")
     T, hq, d = shape
-    dtype = _dtype_code(q, "lily_qk_norm_rope")
+    dtype = _HALVES.get(t)
+    if dtype is None:
+        dtype = _dtype_code(q, "lily_qk_norm_rope")
     if q_out.shape != shape or q_out.dtype is not t or d != op.head_dim:
         raise Q4Error(ERR_INVALID_ARG, f"lily_qk_norm_rope: q {tuple(shape)}, q_out {tuple(q_out.shape)}, "
                                        f"{t}, {q_out.dtype}, heads of {op.head_dim}")
+    dev = q.get_device()
+    if dev < 0 or dev != _current() or q_out.get_device() != dev or op._dev not in (None, dev):
+        _elsewhere("lily_qk_norm_rope")
     qi, qo = q.stride(), q_out.stride()
     if (qi[2] != 1 or qo[2] != 1) and q.numel():
         raise Q4Error(ERR_INVALID_ARG, f"lily_qk_norm_rope: strides {qi}, {qo}")
     if k is None:
         hk, words = 0, (0, 0, 0, 0, 0, 0)
     else:
-        hk = k.shape[1]
-        if k.shape != (T, hk, d) or k_out.shape != k.shape or k.dtype is not t or k_out.dtype is not t:
-            raise Q4Error(ERR_INVALID_ARG, f"lily_qk_norm_rope: k {tuple(k.shape)}, k_out {tuple(k_out.shape)}, "
+        k_shape = k.shape
+        hk = k_shape[1]
+        if k_shape != (T, hk, d) or k_out.shape != k_shape or k.dtype is not t or k_out.dtype is not t:
+            raise Q4Error(ERR_INVALID_ARG, f"lily_qk_norm_rope: k {tuple(k_shape)}, k_out {tuple(k_out.shape)}, "
                                            f"{k.dtype}, {k_out.dtype}")
+        if k.get_device() != dev or k_out.get_device() != dev:
+            _elsewhere("lily_qk_norm_rope: k")
         ki, ko = k.stride(), k_out.stride()
         if (ki[2] != 1 or ko[2] != 1) and k.numel():
             raise Q4Error(ERR_INVALID_ARG, f"lily_qk_norm_rope: strides {ki}, {ko}")
@@ -530,8 +547,10 @@ def lily_qk_norm_rope(op: QKNormRope, q, k, pos, q_out, k_out, stream=None):
         at = _int32(pos, "pos")
         if pos.numel() != T:
             raise Q4Error(ERR_INVALID_ARG, "lily_qk_norm_rope: pos")
+        if pos.get_device() != dev:
+            _elsewhere("lily_qk_norm_rope: pos")
     rc = _call(0, _ROPE(op.c(dtype), T, hq, hk, at, q.data_ptr(), qi[0], qi[1], q_out.data_ptr(), qo[0], qo[1],
-                        *words, _raw_stream(q.get_device()) if stream is None else stream.cuda_stream))
+                        *words, _raw_stream(dev) if stream is None else stream.cuda_stream))
     return rc if rc == OK else _check(rc, "lily_qk_norm_rope")
 
 
@@ -545,6 +564,7 @@ class KV8Cache:
         for a in (k_amax, v_amax):
             _require(tuple(a.shape) == tuple(k.shape[:2]) and str(a.dtype) == "torch.float32"
                      and a.is_contiguous(), "KV8Cache: magnitudes")
+        self._dev = _device_of("KV8Cache", k, v, k_amax, v_amax)
         self.k, self.v, self.k_amax, self.v_amax = k, v, k_amax, v_amax
         self.n_pages, self.kv_heads, self.page, self.head_dim = (int(n) for n in k.shape)
         self._c = lily_kv8_cache(_ptr(k), _ptr(v), _ptr(k_amax), _ptr(v_amax), self.n_pages,
@@ -573,6 +593,7 @@ class KV8Batch:
         n = int(kv_len.numel())
         _require(block_table.dim() == 2 and block_table.shape[0] == n and q_start.numel() == n + 1,
                  "KV8Batch: block_table [batch, pages], q_start [batch + 1], kv_len [batch]")
+        self._dev = _device_of("KV8Batch", block_table, q_start, kv_len)
         self.block_table, self.q_start, self.kv_len = block_table, q_start, kv_len
         self._c = lily_kv8_batch(_int32(block_table, "block_table"), _int32(q_start, "q_start"),
                                  _int32(kv_len, "kv_len"), int(block_table.shape[1]), n,
@@ -585,18 +606,27 @@ class KV8Batch:
 
 
 def _kv8_rows(which, name, cache, batch, k, v, ws, stream, f32):
-    T, h, d = k.shape[0], cache.kv_heads, cache.head_dim
-    dtype = _dtype_code(k, name, f32)
-    if v.dtype is not k.dtype:
+    shape, step, t = k.shape, k.stride(), k.dtype
+    dtype = (_DTYPES if f32 else _HALVES).get(t)
+    if dtype is None:
+        dtype = _dtype_code(k, name, f32)
+    if v.dtype is not t:
         raise Q4Error(ERR_INVALID_ARG, f"{name}: k and v of one type")
-    rc = _call(which, _ROWS(cache._at, batch._at, T, dtype, *_rows(k, T, h, d, "k"),
-                            *_rows(v, T, h, d, "v"), *_space(ws),
-                            _raw_stream(k.get_device()) if stream is None else stream.cuda_stream))
+    dev = cache._dev
+    if dev < 0 or dev != _current() or batch._dev != dev or k.get_device() != dev or v.get_device() != dev:
+        _elsewhere(name)
+    to = v.stride()
+    if (len(shape) != 3 or v.shape != shape or shape[1] != cache.kv_heads or shape[2] != cache.head_dim
+            or (step[2] != 1 or to[2] != 1) and k.numel()):
+        raise Q4Error(ERR_INVALID_ARG, f"{name}: k {tuple(shape)}, strides {step}, v {tuple(v.shape)}, strides {to}")
+    space, size = 0, 0
+    if ws is not None:
+        if ws.get_device() != dev:
+            _elsewhere(f"{name}: workspace")
+        space, size = ws.data_ptr(), ws.nbytes
+    rc = _call(which, _ROWS(cache._at, batch._at, shape[0], dtype, k.data_ptr(), step[0], step[1], v.data_ptr(), to[0],
+                            to[1], space, size, _raw_stream(dev) if stream is None else stream.cuda_stream))
     return rc if rc == OK else _check(rc, name)
-
-
-def _space(ws):
-    return (0, 0) if ws is None else (ws.data_ptr(), ws.nbytes)
 
 
 def lily_kv8_append(cache: KV8Cache, batch: KV8Batch, k, v, ws=None, stream=None):
@@ -622,10 +652,15 @@ def lily_kv8_attention(cache: KV8Cache, batch: KV8Batch, q, out, scale, lse=None
     if len(shape) != 3:
         raise Q4Error(ERR_INVALID_ARG, f"lily_kv8_attention: q {tuple(shape)}")
     T, heads, d = shape
-    dtype = _dtype_code(q, "lily_kv8_attention")
+    dtype = _HALVES.get(t)
+    if dtype is None:
+        dtype = _dtype_code(q, "lily_kv8_attention")
     if out.shape != shape or out.dtype is not t or d != cache.head_dim:
         raise Q4Error(ERR_INVALID_ARG, f"lily_kv8_attention: q {tuple(shape)}, out {tuple(out.shape)}, {t}, "
                                        f"{out.dtype}, heads of {cache.head_dim}")
+    dev = cache._dev
+    if dev < 0 or dev != _current() or batch._dev != dev or q.get_device() != dev or out.get_device() != dev:
+        _elsewhere("lily_kv8_attention")
     qi, qo = q.stride(), out.stride()
     if (qi[2] != 1 or qo[2] != 1) and q.numel():
         raise Q4Error(ERR_INVALID_ARG, f"lily_kv8_attention: strides {qi}, {qo}")
@@ -633,8 +668,15 @@ def lily_kv8_attention(cache: KV8Cache, batch: KV8Batch, q, out, scale, lse=None
     if lse is not None:
         if lse.shape != (T, heads) or lse.dtype is not _float32_t or not lse.is_contiguous():
             raise Q4Error(ERR_INVALID_ARG, "lily_kv8_attention: lse is fp32 [T, q_heads]")
+        if lse.get_device() != dev:
+            _elsewhere("lily_kv8_attention: lse")
         at = lse.data_ptr()
+    space, size = 0, 0
+    if ws is not None:
+        if ws.get_device() != dev:
+            _elsewhere("lily_kv8_attention: workspace")
+        space, size = ws.data_ptr(), ws.nbytes
     rc = _call(3, _ATTENTION(cache._at, batch._at, T, heads, dtype, scale, 1 if causal else 0, window,
-                             q.data_ptr(), qi[0], qi[1], out.data_ptr(), qo[0], qo[1], at, *_space(ws),
-                             _raw_stream(q.get_device()) if stream is None else stream.cuda_stream))
+                             q.data_ptr(), qi[0], qi[1], out.data_ptr(), qo[0], qo[1], at, space, size,
+                             _raw_stream(dev) if stream is None else stream.cuda_stream))
     return rc if rc == OK else _check(rc, "lily_kv8_attention")

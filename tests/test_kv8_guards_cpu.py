@@ -67,3 +67,87 @@ def test_binding_refuses_wide_integers(lib):
             q4.lily_kv8_attention_workspace_bytes(cache, batch, T, heads)
     with pytest.raises(q4.Q4Error):
         q4.lily_rope_turns((1 << 32) + 64)
+
+
+# --------------------------------------------------------------------------- tensors on other devices
+
+class _Stream:
+    cuda_stream = 0
+
+
+def _on(torch, device, *tensors):
+    """CPU tensors that say they are on GPU `device`."""
+    class Placed(torch.Tensor):
+        def get_device(self):
+            return device
+    return [t.as_subclass(Placed) for t in tensors]
+
+
+@pytest.fixture
+def calls(lib, monkeypatch):
+    """What reaches the C ABI, with GPU 0 as the current one and nothing launched."""
+    pytest.importorskip("torch")
+    q4._first_use()
+    seen = []
+    monkeypatch.setattr(q4, "_call", lambda which, words: seen.append(which) or q4.OK)
+    monkeypatch.setattr(q4, "_current", lambda: 0)
+    return seen
+
+
+def _operands(torch, move=None, to=-1):
+    """Operands of every call, all on GPU 0 but for the one named by `move`."""
+    z = lambda *s, dtype=torch.bfloat16: torch.zeros(s, dtype=dtype)
+    i32 = lambda *s: z(*s, dtype=torch.int32)
+    made = dict(k8=z(2, 2, 16, 64, dtype=torch.int8), ka=z(2, 2, dtype=torch.float32), table=i32(1, 2),
+                start=i32(2), length=i32(1), ws=z(1 << 20, dtype=torch.uint8), q=z(1, 4, 64), out=z(1, 4, 64),
+                lse=z(1, 4, dtype=torch.float32), k=z(1, 2, 64), v=z(1, 2, 64), pos=i32(1),
+                turns=z(16, dtype=torch.int64), w=z(64))
+    return {n: _on(torch, to if n == move else 0, t)[0] for n, t in made.items()}
+
+
+def _run(name, o):
+    op = lambda: q4.QKNormRope(64, 32, o["turns"], o["w"], o["w"])
+    cache = lambda: q4.KV8Cache(o["k8"], o["k8"], o["ka"], o["ka"])
+    batch = lambda: q4.KV8Batch(o["table"], o["start"], o["length"], 1, 16)
+    if name == "rope":
+        return q4.lily_qk_norm_rope(op(), o["q"], o["k"], o["pos"], o["out"], o["v"], stream=_Stream)
+    if name == "attention":
+        return q4.lily_kv8_attention(cache(), batch(), o["q"], o["out"], 0.1, lse=o["lse"], ws=o["ws"], stream=_Stream)
+    return getattr(q4, "lily_kv8_" + name)(cache(), batch(), o["k"], o["v"], ws=o["ws"], stream=_Stream)
+
+
+USED = {"rope": ["q", "k", "pos", "out", "v", "turns", "w"],
+        "append": ["k8", "ka", "table", "start", "length", "k", "v", "ws"],
+        "read": ["k8", "ka", "table", "start", "length", "k", "v", "ws"],
+        "attention": ["k8", "ka", "table", "start", "length", "q", "out", "lse", "ws"]}
+
+
+@pytest.mark.parametrize("name", USED)
+def test_tensors_have_to_be_on_the_current_gpu(calls, monkeypatch, name):
+    import torch
+    assert _run(name, _operands(torch)) == q4.OK and len(calls) == 1
+    for move in USED[name]:
+        for to in (-1, 1):
+            with pytest.raises(q4.Q4Error) as e:
+                _run(name, _operands(torch, move, to))
+            assert e.value.status == q4.ERR_INVALID_ARG and len(calls) == 1, (move, to)
+    monkeypatch.setattr(q4, "_current", lambda: 1)
+    with pytest.raises(q4.Q4Error):
+        _run(name, _operands(torch))
+    assert len(calls) == 1
+
+
+@pytest.mark.parametrize("name", USED)
+def test_host_tensors_are_refused(calls, name):
+    import torch
+    o = {n: t.as_subclass(torch.Tensor) for n, t in _operands(torch).items()}
+    with pytest.raises(q4.Q4Error) as e:
+        _run(name, o)
+    assert e.value.status == q4.ERR_INVALID_ARG and not calls
+
+
+def test_a_rotation_without_tensors_takes_any_gpus_heads(calls):
+    import torch
+    o = _operands(torch)
+    op = q4.QKNormRope(64, 0, None)
+    assert q4.lily_qk_norm_rope(op, o["q"], None, None, o["out"], None, stream=_Stream) == q4.OK and len(calls) == 1
