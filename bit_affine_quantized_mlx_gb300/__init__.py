@@ -492,21 +492,22 @@ class QKNormRope:
         if rotary_dim:
             _require(turns is not None and turns.numel() * turns.element_size() == 4 * rotary_dim
                      and turns.is_contiguous(), "QKNormRope: turns is uint64 [rotary_dim / 2]")
-        self._c = lily_qk_rope(self.head_dim, self.rotary_dim, int(bool(interleaved)),
-                               self.dtype or 0, int(bool(normalize)), float(eps),
-                               float(weight_offset), float(rope_scale), _ptr(q_weight),
-                               _ptr(k_weight), _ptr(turns) if rotary_dim else None)
+        # a struct for each type: without weights one operator may serve both, from several threads
+        self._c = {code: lily_qk_rope(self.head_dim, self.rotary_dim, int(bool(interleaved)), code,
+                                      int(bool(normalize)), float(eps), float(weight_offset),
+                                      float(rope_scale), _ptr(q_weight), _ptr(k_weight),
+                                      _ptr(turns) if rotary_dim else None)
+                   for code in (BF16, F16) if self.dtype in (None, code)}
+        self._at = {code: C.addressof(c) for code, c in self._c.items()}
         held = [t for t in (q_weight, k_weight, turns if rotary_dim else None) if t is not None]
         self._dev = _device_of("QKNormRope", *held) if held else None  # None: whatever the heads are on
-        self._at = C.addressof(self._c)
 
     def c(self, dtype):
-        """The C struct's address, for heads of this type."""
-        if self.dtype is None:
-            self._c.dtype = dtype
-        elif self.dtype != dtype:
+        """The address of the C struct for heads of this type."""
+        at = self._at.get(dtype)
+        if at is None:
             raise Q4Error(ERR_INVALID_ARG, "lily_qk_norm_rope: weights and heads of two types")
-        return self._at
+        return at
 
 
 def lily_qk_norm_rope(op: QKNormRope, q, k, pos, q_out, k_out, stream=None):

@@ -151,3 +151,21 @@ def test_a_rotation_without_tensors_takes_any_gpus_heads(calls):
     o = _operands(torch)
     op = q4.QKNormRope(64, 0, None)
     assert q4.lily_qk_norm_rope(op, o["q"], None, None, o["out"], None, stream=_Stream) == q4.OK and len(calls) == 1
+
+
+# --------------------------------------------------------------------------- one operator, two types
+
+def test_one_rotation_serves_two_types_at_once(lib):
+    """The struct that a call was given stays as it is when another thread takes the other type's."""
+    torch = pytest.importorskip("torch")
+    read = lambda at: q4.lily_qk_rope.from_address(at).dtype
+    op = q4.QKNormRope(64, 32, torch.zeros(16, dtype=torch.int64))
+    first, second = op.c(q4.BF16), op.c(q4.F16)
+    assert (read(first), read(second)) == (q4.BF16, q4.F16)
+    assert (op.c(q4.BF16), op.c(q4.F16)) == (first, second)
+    for code, dtype in ((q4.BF16, torch.bfloat16), (q4.F16, torch.float16)):
+        op = q4.QKNormRope(64, 32, torch.zeros(16, dtype=torch.int64), torch.ones(64, dtype=dtype))
+        assert read(op.c(code)) == code
+        with pytest.raises(q4.Q4Error) as e:
+            op.c(q4.F16 if code == q4.BF16 else q4.BF16)
+        assert e.value.status == q4.ERR_INVALID_ARG
