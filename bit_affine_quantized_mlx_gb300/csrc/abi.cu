@@ -89,7 +89,7 @@ static int check_cache(const lily_kv8_cache *C) {
 static int check_bounds(const lily_kv8_batch *b, int T) {
   if (!b || T < 0 || b->batch < 0 || b->table_pages < 0 || b->max_q < 0 || b->max_kv < 0)
     return LILY_Q4_ERR_INVALID_ARG;
-  if (b->batch > 4096) return LILY_Q4_ERR_UNSUPPORTED;
+  if (b->batch > kMaxBatch) return LILY_Q4_ERR_UNSUPPORTED;
   if (T > 0 && (b->batch == 0 || b->table_pages == 0 || b->max_q == 0)) return LILY_Q4_ERR_INVALID_ARG;
   return LILY_Q4_OK;
 }

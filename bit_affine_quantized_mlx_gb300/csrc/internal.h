@@ -1,5 +1,6 @@
 // Internal declarations shared by the library's translation units (host side).
 #pragma once
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 #include <cuda_runtime.h>
@@ -112,6 +113,7 @@ int launch_kv8_append(const lily_kv8_cache &C, const lily_kv8_batch &b, int T, i
                       const Rows &k, const Rows &v, void *ws, cudaStream_t st);
 int launch_kv8_read(const lily_kv8_cache &C, const lily_kv8_batch &b, int T, int dtype, const Rows &k,
                     const Rows &v, void *ws, cudaStream_t st);
+constexpr int kMaxBatch = 4096;  // sequences of a call
 struct Batch;
 Batch make_batch(const lily_kv8_cache &C, const lily_kv8_batch &b, int T);
 struct AttnShape {
@@ -144,15 +146,18 @@ inline cudaError_t launch_pdl(void (*fn)(KArgs...), dim3 grid, dim3 block, size_
   return cudaLaunchKernelEx(&cfg, fn, args...);
 }
 
-// Opt a kernel in to `bytes` of dynamic shared memory, once a device (allowed[] is the kernel's).
-template <typename F>
-inline cudaError_t allow_smem(F *fn, size_t bytes, size_t (&allowed)[64]) {
+// Opt a kernel in to BYTES of dynamic shared memory, once a device (done[] is the kernel's).  The most that
+// any of its launches takes, a constant: threads that come here together all set the same limit, so
+// that none can lower what another relies on.
+template <size_t BYTES, typename F>
+inline cudaError_t allow_smem(F *fn, std::atomic<bool> (&done)[64]) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  if (dev >= 0 && dev < 64 && allowed[dev] >= bytes) return cudaSuccess;
-  e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-  if (e == cudaSuccess && dev >= 0 && dev < 64) allowed[dev] = bytes;
+  const bool known = dev >= 0 && dev < 64;
+  if (known && done[dev].load(std::memory_order_acquire)) return cudaSuccess;
+  e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)BYTES);
+  if (e == cudaSuccess && known) done[dev].store(true, std::memory_order_release);
   return e;
 }
 

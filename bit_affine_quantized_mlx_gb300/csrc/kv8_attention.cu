@@ -101,6 +101,13 @@ constexpr int ring_bytes(int D, int NT) {
   return ring > out ? ring : (out + 127) / 128 * 128;
 }
 
+// Bytes of a block's shared memory.
+constexpr size_t decode_smem(int D, int NT, int batch) {
+  const int RT = 8 * NT, ng = kTurnBytes / D / 16;
+  return kDecWarps * ring_bytes(D, NT) + RT * (D * 2 + 16 + 16) +
+         4 * (kDecWarps * kDecStages * 2 * ng + RT + 2 * kDecWarps * RT + 4 + batch + 1);
+}
+
 // Blocks an SM: three where 168 registers hold a tile of 8 rows (64 sequences up to 32k tokens of 8 heads
 // of 128: 383 us with two, 352 with three), else two.
 constexpr int decode_blocks(int D, int NT) { return D <= 128 && NT == 1 ? 3 : 2; }
@@ -695,9 +702,7 @@ static DecodePlan decode_plan(const lily_kv8_cache &C, const lily_kv8_batch &b, 
   p.join = tiles == 1 ? 0 : p.grid / items >= 32 ? kJoinMost : 128;
   p.items = (int)std::min<int64_t>(items, p.grid);
   p.rows = (int)std::min<int64_t>(RT, rows);
-  const int ng = kTurnBytes / D / 16;
-  p.smem = kDecWarps * ring_bytes(D, p.nt) + RT * (D * 2 + 16 + 16) +
-           4 * (kDecWarps * kDecStages * 2 * ng + RT + 2 * kDecWarps * RT + 4 + b.batch + 1);
+  p.smem = decode_smem(D, p.nt, b.batch);
   size_t off = kAlign;
   p.off_jobs = off;
   off = align_up(off + (size_t)p.grid * 2 * sizeof(int4));
@@ -711,8 +716,8 @@ static DecodePlan decode_plan(const lily_kv8_cache &C, const lily_kv8_batch &b, 
 template <int D, int NT>
 static cudaError_t launch_decode_shape(const AttnArgs &a, const DecodePlan &p, int bf16, cudaStream_t st) {
   auto kernel = kv8_decode_kernel<D, NT>;
-  static size_t allowed[64];
-  cudaError_t e = allow_smem(kernel, p.smem, allowed);
+  static std::atomic<bool> allowed[64];
+  cudaError_t e = allow_smem<decode_smem(D, NT, kMaxBatch)>(kernel, allowed);
   if (e != cudaSuccess) return e;
   e = launch_pdl(kernel, dim3(p.grid), dim3(kDecThreads), p.smem, st, a, bf16);
   if (e != cudaSuccess || !p.join) return e;

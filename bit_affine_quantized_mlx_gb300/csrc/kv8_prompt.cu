@@ -930,8 +930,8 @@ PromptPlan prompt_plan(const lily_kv8_cache &C, const lily_kv8_batch &b, int T, 
 template <int D>
 static cudaError_t launch_prompt_dim(const AttnArgs &a, const PromptPlan &p, int bf16, cudaStream_t st) {
   using P = PromptShape<D>;
-  static size_t allowed[64];
-  cudaError_t e = allow_smem(kv8_prompt_kernel<D>, P::SMEM, allowed);
+  static std::atomic<bool> allowed[64];
+  cudaError_t e = allow_smem<P::SMEM>(kv8_prompt_kernel<D>, allowed);
   if (e != cudaSuccess) return e;
   e = launch_pdl(kv8_prompt_kernel<D>, dim3(p.items, p.splits), dim3(P::THREADS), P::SMEM, st, a, bf16, p.splits);
   if (e != cudaSuccess || p.splits == 1) return e;

@@ -215,3 +215,41 @@ def test_status_reports_an_index_error_beside_a_time_out(torch):
     q4.lily_q4_selftest_timeout(ws, 1)  # a bounded wait on a barrier that nothing completes
     q4.lily_kv8_read(s.cache, s.batch, ko, ko.clone(), ws=ws)
     assert [q4.lily_q4_workspace_status(ws) for _ in range(3)] == [q4.ERR_TIMEOUT, q4.ERR_INDEX, q4.OK]
+
+
+# --------------------------------------------------------------------------- threads
+
+def test_small_and_large_batches_from_several_threads(torch):
+    """A kernel's first launches, with little and with much shared memory, from threads on streams of their own."""
+    import threading
+    for D in (64, 128, 256):
+        for group in (1, 9, 17):
+            jobs = []
+            for batch in (1, 4096, 2, 3000):
+                s = Setup(torch, [20] * batch, [1] * batch, 1, D, 16, "float16", seed=batch).upload()
+                jobs.append((s, s.rows(group), torch.cuda.Stream()))
+            failed, start = [], threading.Barrier(len(jobs), timeout=60)
+
+            def work(s, q, stream):
+                try:
+                    q = q.cuda()
+                    out, ws = torch.empty_like(q), q4.new_workspace(
+                        q4.lily_kv8_attention_workspace_bytes(s.cache, s.batch, s.T, group))
+                    torch.cuda.synchronize()
+                    start.wait()
+                    for _ in range(20):
+                        q4.lily_kv8_attention(s.cache, s.batch, q, out, 0.1, ws=ws, stream=stream)
+                    torch.cuda.synchronize()
+                    assert q4.lily_q4_workspace_status(ws) == q4.OK
+                    for b in (0, len(s.len) - 1):
+                        o, _, tol, _ = expected(torch, s, q.cpu(), b, 0.1)
+                        _close(_f64(out[b:b + 1]), o, tol, f"sequence {b} of {len(s.len)}")
+                except Exception as e:  # reported by the main thread
+                    failed.append(e)
+
+            threads = [threading.Thread(target=work, args=j) for j in jobs]
+            for t in threads:
+                t.start()
+            for t in threads:
+                t.join()
+            assert not failed, failed
