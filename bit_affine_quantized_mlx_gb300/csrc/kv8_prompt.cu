@@ -909,7 +909,8 @@ PromptPlan prompt_plan(const lily_kv8_cache &C, const lily_kv8_batch &b, int T, 
   // than SMs were slower: 9 sequences of 49 tokens after up to 42,909, 5 heads of 128: 66 us with one
   // share an SM, 67, 73 and 86 with two, three and four; 85 of 7 tokens after up to 2576, 32 / 2 heads
   // of 256: 80 whole, 93 in halves.
-  const int64_t most = items < sms ? sms : 8 * sms;  // parts in the workspace
+  // parts in the workspace: more than an SM's each only where the second rule can come to it
+  const int64_t most = items < sms || per_seq < sms ? sms : 8 * sms;
   auto time = [&](int64_t n) { return (items * n + sms - 1) / sms * (tiles / (double)n + 4); };
   p.items = (int)items;
   p.splits = (int)std::max<int64_t>(1, std::min<int64_t>(sms / items, tiles / 2));

@@ -169,3 +169,31 @@ def test_one_rotation_serves_two_types_at_once(lib):
         with pytest.raises(q4.Q4Error) as e:
             op.c(q4.F16 if code == q4.BF16 else q4.BF16)
         assert e.value.status == q4.ERR_INVALID_ARG
+
+
+# --------------------------------------------------------------------------- workspaces
+
+def test_prompt_workspace_has_room_for_parts_that_there_can_be(lib):
+    """Keys are split more than once an SM only where one sequence fills the SMs.  Many short prompts need no
+    more than a part an SM: 152 of 256 rows of 128 outputs, a maximum and a sum, in fp32."""
+    part = 256 * (128 + 2) * 4
+    many = _size(lib, _cache(kv_heads=8), _batch(batch=100, max_q=300, max_kv=5000, table_pages=100), 30000, 32)
+    one = _size(lib, _cache(kv_heads=8), _batch(batch=1, max_q=4096, max_kv=50000, table_pages=1000), 4096, 32)
+    assert 152 * part <= many < 2 * 152 * part
+    assert 8 * 152 * part <= one < 9 * 152 * part
+
+
+def test_smaller_calls_need_no_more_space(lib):
+    """Over a grid of bounds: fewer sequences, rows, tokens or keys never need more than the larger call."""
+    grid = [(b, n, t, kv) for b in (1, 3, 20, 300) for n in (1, 7, 33, 97, 300, 2500) for t in (1, 40, 900, 20000)
+            for kv in (20, 600, 9000, 200000)]
+    for heads, group, D in ((1, 1, 64), (2, 8, 256), (8, 4, 128), (1, 48, 64), (16, 1, 256)):
+        size = {}
+        for b, n, t, kv in grid:
+            size[b, n, t, kv] = _size(lib, _cache(kv_heads=heads, head_dim=D),
+                                      _batch(batch=b, max_q=n, max_kv=kv, table_pages=1 << 14), t, heads * group)
+        for at in grid:
+            for axis in range(4):
+                less = [g for g in grid if g[axis] < at[axis] and all(g[i] == at[i] for i in range(4) if i != axis)]
+                if less:
+                    assert max(size[g] for g in less) <= size[at], (heads, group, D, at, axis)
