@@ -204,6 +204,28 @@ def test_tables_wider_than_positions(torch, new):
     check_attention(torch, s, 4, 0.1)
 
 
+@pytest.mark.parametrize("page,length", [(16, (1 << 29) - 3), (128, (1 << 31) - 65600)])
+def test_last_tokens_of_a_far_sequence(torch, page, length):
+    """Append and read at positions near the end of a table of 2^25 and 2^24 entries."""
+    new, D = 5, 64
+    s = Setup(torch, [0], [new], 1, D, page, "bfloat16").upload()
+    table = torch.full((1, 1 << 25 if page == 16 else 1 << 24), -9, dtype=torch.int32, device="cuda")
+    first = (length - new) // page
+    table[0, first], table[0, (length - 1) // page] = 1, 2 if (length - 1) // page != first else 1
+    i32 = lambda *a: torch.tensor(a, dtype=torch.int32, device="cuda")
+    batch = q4.KV8Batch(table, i32(0, new), i32(length), new, length)
+    s.cache = q4.KV8Cache.new(4, 1, page, D)
+    x = s.rows(1).cuda()
+    k, v = (torch.empty((new, 1, D), dtype=torch.float32, device="cuda") for _ in "kv")
+    ws = q4.new_workspace(256)
+    q4.lily_kv8_append(s.cache, batch, x, x, ws=ws)
+    q4.lily_kv8_read(s.cache, batch, k, v, ws=ws)
+    assert q4.lily_q4_workspace_status(ws) == q4.OK
+    # a code is off by half a step of the page's largest magnitude
+    _close(_f64(k), _f64(x), np.abs(_f64(x)).max() * (0.5 / 127 + 2.0 ** -22), "keys")
+    assert torch.equal(k, v)
+
+
 # --------------------------------------------------------------------------- status
 
 def test_status_reports_an_index_error_beside_a_time_out(torch):
