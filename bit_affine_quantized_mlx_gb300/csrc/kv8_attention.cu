@@ -35,9 +35,9 @@
 // term that any one key adds to the output) and multiplies the codes; the softmax's sum adds 2^(x - m) / a in
 // fp32 (times a power of two, see kv8_device.cuh).
 //
-// Measured on one GB300: 64 sequences of up to 32,768 tokens (1.12M in all), 32 / 8 heads of 128: 349 us
+// Measured on one GB300: 64 sequences of up to 32,768 tokens (1.12M in all), 32 / 8 heads of 128: 348 us
 // (6.6 TB/s of codes, 97% of the measured copy rate); one sequence of 262,144 tokens, 16 / 2 heads of 256:
-// 50.5 us with the join (5.3 TB/s, 78%: two blocks an SM, and 8 us of join); one of 777 tokens: 7.6 us, the
+// 50.2 us with the join (5.3 TB/s, 79%: two blocks an SM, and 8 us of join); one of 777 tokens: 7.3 us, the
 // chain of dependent reads (lengths, pages, codes, parts) of two launches.
 #include <algorithm>
 
@@ -49,7 +49,8 @@ namespace lq4 {
 constexpr int kDecThreads = 128, kDecWarps = 4, kDecStages = 2;
 // What beginning an item costs a block (its lengths, pages, queries and the join of its warps), in tiles:
 // items are that much longer when they are shared out, so that a block with the ends of two has
-// fewer tiles (16 x 3 tokens over 4096 keys, 96 items of 17 tiles: 18.5 us without).
+// fewer tiles.  At 0, 1, 2, 3 and 4: 16 x 3 tokens over 4096 keys, 96 items of 17 tiles: 20.5, 19.3, 19.2, 19.2
+// and 21.1 us; one sequence of 777 keys 7.6, 7.7, 7.3, 7.5, 7.6; 64 sequences of up to 32,768: 352, 349, 348, 349, 350.
 constexpr int kStart = 2;
 constexpr int kTurnBytes = 4096;  // of keys, and of values, a warp and turn
 // The reference of a row's weights below its largest exponent: weights up to 2^14, and room for rounding, in fp16.
@@ -735,12 +736,12 @@ static cudaError_t launch_decode_dim(const AttnArgs &a, const DecodePlan &p, int
 }
 
 // Rows of a sequence and key/value head from which the tcgen05 form runs.  Measured with both forms
-// (us, split / tcgen05): 32 sequences of 4096 keys, 8 heads of 128: 16 rows 76 / 137, 32 rows
-// 147 / 138, 48 rows 264 / 138; 4 heads of 64: 16 rows 32 / 54, 32 rows 52 / 55, 64 rows 87 / 55;
-// 2 heads of 256: 32 rows 75 / 66, 64 rows 124 / 67; one sequence of 32768 keys, 8 heads of 128:
-// 32 rows 41 / 45, 48 rows 64 / 45.  With heads of 256 and so few sequences that the tcgen05 form has to
+// (us, split / tcgen05): 32 sequences of 4096 keys, 8 heads of 128: 16 rows 71 / 123, 32 rows
+// 111 / 123, 48 rows 196 / 124; 4 heads of 64: 16 rows 31 / 45, 32 rows 49 / 46, 64 rows 84 / 46;
+// 2 heads of 256: 32 rows 66 / 61, 64 rows 118 / 63; one sequence of 32768 keys, 8 heads of 128:
+// 32 rows 33 / 41, 48 rows 56 / 41.  With heads of 256 and so few sequences that the tcgen05 form has to
 // split the keys, its parts' outputs (128 rows of 256 each) cost more than reading the codes again:
-// one sequence, 2 heads, 32768 keys: 64 rows 40 / 60, 96 rows 56 / 61, 128 rows 62 / 62.
+// one sequence, 2 heads, 32768 keys: 64 rows 36 / 56, 96 rows 51 / 57, 128 rows 62 / 58.
 static int prompt_rows(const lily_kv8_cache &C, const lily_kv8_batch &b) {
   const int sms = sm_count() > 0 ? sm_count() : 152;
   return C.head_dim == 256 && (int64_t)b.batch * C.kv_heads * 4 <= sms ? 97 : 33;

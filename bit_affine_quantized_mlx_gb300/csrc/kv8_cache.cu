@@ -66,7 +66,7 @@ __device__ __forceinline__ uint32_t umax16x2(uint32_t a, uint32_t b) { return __
 
 // A position before the first or, which a sequence within its bounds has none of, beyond the table (its
 // tokens counted below 2^31).  Without the second half the compiler gives the append of 64-thread teams 88
-// registers instead of 80: 11.5k tokens of 8 heads of 128 in pages of 32 took 20.1 us, not 19.1.
+// registers instead of 80: 11.5k tokens of 8 heads of 128 in pages of 32, repeated, took 20.1 us, not 19.1.
 __device__ __forceinline__ bool off_table(const Batch &B, int pos) {
   return pos < 0 || pos >= min(B.table_pages, INT_MAX >> B.page_shift) * B.page;
 }

@@ -29,14 +29,15 @@
 // moving it rescales O in tensor memory.  Head_dim 64 and 128 need no maximum before
 // the weights then: a tile is done in one pass to the reference there is, and done again where sixteen of a
 // row's weights come to more than 65504 (ragged prompts below: 657 us with a pass for the maximum, 608 with
-// the maximum beside the weights, 583 with their sums, which are there anyway, as the sign).  The pass
+// the maximum beside the weights, 583 with a sum, which is there anyway, as the sign).  The pass
 // holds a row's 64 words of weights until it is known to stand, so the softmax warps take registers
-// from the issuing warp's group (160 a thread and 64; 168 and 40: 586 us; 152 and 80: 620 us; 144 and
-// 96: 609 us).  Head_dim 256 has no registers for it.
+// from the issuing warp's group (160 a thread and 64: those 583 us; 168 and 40: 586; 152 and 80: 620; 144 and
+// 96: 609).  Head_dim 256 has no registers for it.
 //
-// Measured on one GB300: 5 ragged prompts, 6.6k tokens over up to 8k keys each, 32 / 8 heads of 128: 583 us
-// (1,092 TFLOP/s, 57% of the measured bf16 rate); a 4096-token chunk after 28,672, 16 / 2 heads of 256:
-// 1.95 ms (1,058 TFLOP/s, 55%).  What bounds it: at 128, the chain of one row tile (scores 540 cycles,
+// Measured on one GB300: 5 ragged prompts, 6.6k tokens over up to 8k keys each, 32 / 8 heads of 128: 578 us
+// (1,101 TFLOP/s, 57% of the measured bf16 rate); a 4096-token chunk after 28,672, 16 / 2 heads of 256:
+// 1.95 ms (1,058 TFLOP/s, 55%); 5 prompts of 1500 tokens after 3000, 16 / 4 heads of 64: 199 us (30%: its
+// 450M exponentials alone take about 90 us).  What bounds it: at 128, the chain of one row tile (scores 540 cycles,
 // weights about 1,750, product 870, hand-overs 700) against the other's, and the issue of
 // the softmax's instructions (an eighth of the exponentials as polynomials instead: 657 -> 679 us, half
 // of them 748); at 256 conversion and products about equally (without conversion 1.61 ms, with a

@@ -275,7 +275,8 @@ LILY_Q4_API int lily_q4_selftest_timeout(void *ws, size_t ws_bytes, int32_t whic
  *
  * What runs between two MoE layers of a decode step or a prompt chunk: the norm of every
  * query and key head with its position rotation, and grouped-query attention over a paged
- * key/value cache held in 8 bits (the fork page, "The model", keeps attention at 8 bits).
+ * key/value cache held in 8 bits.  The pages that this library follows state no such cache: its
+ * format is the library's own.
  *
  * Conventions of these calls, besides those at the top of this file:
  *  - Activations are [tokens][heads][head_dim] with the last axis dense and two strides in
@@ -294,7 +295,7 @@ LILY_Q4_API int lily_q4_selftest_timeout(void *ws, size_t ws_bytes, int32_t whic
 
 #define LILY_ROPE_NONE 0
 #define LILY_ROPE_LINEAR 1 /* every frequency divided by `factor` */
-#define LILY_ROPE_YARN 2   /* the published per-frequency ramp, see lily_rope_turns */
+#define LILY_ROPE_YARN 2   /* the paper's per-frequency ramp, linear in turns: see lily_rope_turns */
 
 /*
  * lily_rope_turns -- host only: the rotation table of lily_qk_norm_rope.
@@ -303,7 +304,10 @@ LILY_Q4_API int lily_q4_selftest_timeout(void *ws, size_t ws_bytes, int32_t whic
  * `factor`.  YARN keeps frequencies that make at least `fast` turns within `original_len`
  * positions, divides those that make at most `slow` by `factor`, and blends linearly in the
  * number of turns between them (its usual bounds are slow = 1, fast = 32; its attention
- * factor 0.1 ln(factor) + 1 goes into lily_qk_rope.rope_scale).
+ * factor 0.1 ln(factor) + 1 goes into lily_qk_rope.rope_scale).  That is the paper's ramp.  Many
+ * checkpoint loaders blend linearly in the pair's index i instead, between bounds rounded to whole
+ * pairs, which gives other frequencies inside the blend: for a checkpoint that was trained or is
+ * served that way, fill turns[] from those frequencies by the next sentence.
  * turns[i] = f_i / (2 pi) of a turn as an unsigned 64-bit fraction (2^64 = one whole turn;
  * whole turns are dropped).  pos * turns[i] mod 2^64 is then the angle without the loss that
  * a 32-bit product has at far positions: its error is pos * 2^-54 turns at most (the
@@ -361,9 +365,12 @@ typedef struct {
  * sequence's last page are not read.  max_q and max_kv are the host's upper bounds of n_b and
  * kv_len[b]; they size the launch.
  * A sequence whose row range or length is out of bounds (n_b > max_q, kv_len > max_kv or more
- * than table_pages pages, rows beyond T; above 2^31 - 65536 in any case) is skipped and a page number outside the cache is
- * passed over (its tokens are not written, read as zero, and masked in attention); either is
- * recorded for lily_q4_workspace_status as LILY_Q4_ERR_INDEX. */
+ * than table_pages pages, or above 2^31 - 65536 in any case, rows beyond T) is skipped and a page
+ * number outside the cache is passed over (its tokens are not written, read as zero, and masked in
+ * attention); either is recorded for lily_q4_workspace_status as LILY_Q4_ERR_INDEX.  q_start has to
+ * ascend: where it does not, that is recorded too and rows may be left out or taken twice.
+ * Rows before position 0 (n_b > kv_len) see nothing in attention; append and read leave them out and
+ * record them. */
 typedef struct {
   const int32_t *block_table; /* [batch][table_pages] */
   const int32_t *q_start;     /* [batch + 1] */
@@ -392,8 +399,8 @@ LILY_Q4_API int lily_kv8_append(const lily_kv8_cache *cache, const lily_kv8_batc
 
 /*
  * lily_kv8_read -- the values of the batch's tokens, q * amax / 127 (in fp32: q amax is exact,
- * times 1/127, 2^-23 relative) rounded to dtype (LILY_BF16, LILY_F16 or LILY_F32): the inverse of lily_kv8_append, for moving a prefix to
- * another cache or checking one.
+ * times 1/127, 2^-23 relative, for every finite amax) rounded to dtype (LILY_BF16, LILY_F16 or
+ * LILY_F32): the inverse of lily_kv8_append, for moving a prefix to another cache or checking one.
  */
 LILY_Q4_API int lily_kv8_read(const lily_kv8_cache *cache, const lily_kv8_batch *batch, int32_t T,
                               int32_t dtype, void *k_out, int64_t k_ts, int64_t k_hs, void *v_out,
