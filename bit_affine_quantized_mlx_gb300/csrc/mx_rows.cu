@@ -103,7 +103,7 @@ __device__ __forceinline__ void scale_exactly(float (&s)[8], const float (&w)[8]
     const float hi = __fmul_rn(p, r.hi);
     const float lo = __fmaf_rn(p_lo, r.hi, __fmaf_rn(p, r.lo, __fmaf_rn(p, r.hi, -hi)));
     const float y = __fadd_rn(hi, lo);
-    s[j] = to_odd(y, __fsub_rn(lo, __fsub_rn(y, hi)));
+    s[j] = hi == 0.f ? hi : to_odd(y, __fsub_rn(lo, __fsub_rn(y, hi)));  // (a sum of zeros would lose the sign)
   }
 }
 // The same as 16-bit numbers, by plain fp32 products with a root a little smaller and one a little larger: rounding keeps the
