@@ -4,9 +4,9 @@
 // thread takes eight neighbours (16 bytes of a 16-bit row), so a block of 32 is in four neighbouring
 // lanes and its largest magnitude takes two exchanges.
 //
-// Measured on one GB300: 8192 rows of 2048 with the addition and all outputs 26.1 us (5.8 TB/s, 85% of the measured copy rate);
-// without the addition, to 8 bits alone, 18.0 us (2.8 TB/s: bound by the issue of some 30 instructions an element);
-// one row 1.9 us (a launch).  151,936 x 2048 of bf16 to 4 bits 126 us (6.2 TB/s), back 114 us (6.9 TB/s).
+// Measured on one GB300: 8192 rows of 2048 with the addition and all outputs 26.8 us (5.6 TB/s, 83% of the measured copy rate);
+// without the addition, to 8 bits alone, 19.6 us (2.6 TB/s: bound by the issue of some 30 instructions an element);
+// one row 2.0 us (a launch).  151,936 x 2048 of bf16 to 4 bits 126 us (6.2 TB/s), back 114 us (6.9 TB/s).
 #include <algorithm>
 
 #include "mx_device.cuh"
@@ -71,17 +71,21 @@ __device__ __forceinline__ Pair warp_total(Pair v) {
   return Pair{__fmul_rn(most, back), __fmul_rn(__fadd_rn(__uint2float_rn(sum - (uint32_t)most), rest), back)};
 }
 // 1 / sqrt(total / H + eps)
-__device__ __forceinline__ Pair pair_rsqrt(Pair total, const NormArgs &a) {
+__device__ __forceinline__ Pair pair_rsqrt(Pair total, float eps, const NormArgs &a) {
   Pair m;
   m.hi = __fmul_rn(total.hi, a.inv_hi);
   m.lo = __fmaf_rn(total.hi, a.inv_hi, -m.hi);
   m.lo = __fmaf_rn(total.hi, a.inv_lo, __fmaf_rn(total.lo, a.inv_hi, m.lo));
-  m = pair_add(m, Pair{a.eps, 0.f});
+  m = pair_add(m, Pair{eps, 0.f});
+  // an even power of two goes to the end, so that the root's square has a remainder whatever eps is
+  const int even = ((int)(__float_as_uint(m.hi) >> 23) - 127) & ~1;
+  const float by = __uint_as_float((uint32_t)(127 - even) << 23), back = __uint_as_float((uint32_t)(127 - even / 2) << 23);
+  m.hi = __fmul_rn(m.hi, by), m.lo = __fmul_rn(m.lo, by);
   // r (1 + e / 2), e = 1 - m r^2: what is left is 3/8 e^2, 2^-43 at the root's accuracy of 2^-22
   const float r = rsqrtf(m.hi), r2 = __fmul_rn(r, r), r2_lo = __fmaf_rn(r, r, -r2);
   float e = __fmaf_rn(-m.hi, r2, 1.f);
   e = __fmaf_rn(-m.hi, r2_lo, __fmaf_rn(-m.lo, r2, e));
-  return Pair{r, __fmul_rn(r, __fmul_rn(0.5f, e))};
+  return Pair{__fmul_rn(r, back), __fmul_rn(__fmul_rn(r, back), __fmul_rn(0.5f, e))};
 }
 // hi + lo as the fp32 number to round further: where hi is even and lo is not 0, hi's odd neighbour on lo's side.
 // An odd number is no tie of a shorter format, and lies on the same side of each as hi + lo.
@@ -132,9 +136,20 @@ __device__ __forceinline__ uint4 scale_eight(const uint4 &s, const uint4 &w, flo
   return one;
 }
 
+// Where a sum of squares is out of what the pairs hold, the row is multiplied with a power of two, eps with its square, and
+// summed again: the norm is the same, and bf16 holds such rows exactly, but for what is 2^-166 of the largest and less.
+// In range nothing counts that fp32 cannot hold: what a square and its remainder lose is 2^-149 at most, of up to 2^15 squares
+// 2^-54 of a sum of 2^-80 or, whatever the sum is, 2^-49 of an eps of 2^-100.  (Sums of fp16 squares are 2^-48 to 2^47.)  Large rows go
+// to 2^40 instead of 1, so that their small elements do not run out of bits.  (What asking takes: 8192 rows of 2048 with all
+// outputs 26.5 -> 26.8 us, to 8 bits alone 18.9 -> 19.6.)
+__device__ __forceinline__ bool out_of_range(Pair total, float eps) {
+  return !(total.hi < 0x1p100f) || (eps < 0x1p-100f && total.hi < 0x1p-80f);
+}
+
 // R threads a row (a warp or more), NV times eight elements each.
 template <typename Ty, int NV>
 __global__ void __launch_bounds__(1024) add_rms_norm_kernel(NormArgs a, int R) {
+  constexpr bool kFar = std::is_same<Ty, Bf16>::value;  // rows that can be out_of_range
   __shared__ Pair s_part[32];
   pdl_wait();
   next_may_start();
@@ -172,31 +187,60 @@ __global__ void __launch_bounds__(1024) add_rms_norm_kernel(NormArgs a, int R) {
       most = __vmaxu2(most, largest_two(raw[i]));
     }
   }
-  // a power of two, so that taking it off in the end is exact too
-  const float top = __uint_as_float((__float_as_uint(largest_of<Ty>(most)) & 0x7F800000u) + 0x800000u), first = __fmul_rn(top, top);
-  uint64_t sums = pack2(first, first), rest = 0;  // of even and of odd elements
+  Pair total;
+  float eps = a.eps;
+  for (bool once = true;; once = false) {
+    // a power of two, so that taking it off in the end is exact too
+    const float top = __uint_as_float((__float_as_uint(largest_of<Ty>(most)) & 0x7F800000u) + 0x800000u), first = __fmul_rn(top, top);
+    uint64_t sums = pack2(first, first), rest = 0;  // of even and of odd elements
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    float s[8];
-    unpack8<Ty>(raw[i], s);
+    for (int i = 0; i < NV; ++i) {
+      float s[8];
+      unpack8<Ty>(raw[i], s);
 #pragma unroll
-    for (int j = 0; j < 8; j += 2) {
-      const uint64_t two = pack2(s[j], s[j + 1]), sum = fma2(two, two, sums);
-      rest = add2(rest, fma2(two, two, sub2(sums, sum)));
-      sums = sum;
+      for (int j = 0; j < 8; j += 2) {
+        const uint64_t two = pack2(s[j], s[j + 1]), sum = fma2(two, two, sums);
+        rest = add2(rest, fma2(two, two, sub2(sums, sum)));
+        sums = sum;
+      }
+    }
+    const float2 h = unpack2(sub2(sums, pack2(first, first))), l = unpack2(rest);
+    total = warp_total(pair_add(Pair{h.x, l.x}, Pair{h.y, l.y}));
+    bool far = kFar && once && out_of_range(total, eps);
+    if (R > 32) {
+      if ((threadIdx.x & 31) == 0) s_part[threadIdx.x >> 5] = total;
+      if (kFar) far = __syncthreads_or(far);
+      else __syncthreads();
+      const int warps = R >> 5, places = 1 << (32 - __clz(warps - 1)), place = threadIdx.x & (places - 1);
+      total = place < warps ? s_part[which * warps + place] : Pair{0.f, 0.f};
+      for (int o = places / 2; o; o >>= 1)
+        total = pair_add(total, Pair{__shfl_xor_sync(~0u, total.hi, o), __shfl_xor_sync(~0u, total.lo, o)});
+    }
+    if (!far) break;
+    uint32_t biggest = __reduce_max_sync(~0u, max(most & 0xFFFFu, most >> 16));
+    if (R > 32) {
+      __syncthreads();
+      if ((threadIdx.x & 31) == 0) s_part[threadIdx.x >> 5].hi = __uint_as_float(biggest);
+      __syncthreads();
+      for (int w = 0; w < R >> 5; ++w) biggest = max(biggest, __float_as_uint(s_part[which * (R >> 5) + w].hi));
+      __syncthreads();
+    }
+    // the exponent of the largest magnitude or of eps's root, whichever is larger, to 0 or (see out_of_range) to 40
+    const int of_eps = eps > 0.f ? ((int)(__float_as_uint(eps) >> 23) - 126) >> 1 : -127, e = max((int)(biggest >> 7) - 127, of_eps);
+    const float by = biggest >= 0x7F80u ? 1.f : __uint_as_float((uint32_t)(127 + (e > 0 ? 40 - e : min(126, -e))) << 23);
+    eps = __fmul_rn(__fmul_rn(eps, by), by);
+    most = 0;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      float s[8];
+      unpack8<Ty>(raw[i], s);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s[j] = __fmul_rn(s[j], by);
+      raw[i] = pack8<Ty>(s);
+      most = __vmaxu2(most, largest_two(raw[i]));
     }
   }
-  const float2 h = unpack2(sub2(sums, pack2(first, first))), l = unpack2(rest);
-  Pair total = warp_total(pair_add(Pair{h.x, l.x}, Pair{h.y, l.y}));
-  if (R > 32) {
-    if ((threadIdx.x & 31) == 0) s_part[threadIdx.x >> 5] = total;
-    __syncthreads();
-    const int warps = R >> 5, places = 1 << (32 - __clz(warps - 1)), place = threadIdx.x & (places - 1);
-    total = place < warps ? s_part[which * warps + place] : Pair{0.f, 0.f};
-    for (int o = places / 2; o; o >>= 1)
-      total = pair_add(total, Pair{__shfl_xor_sync(~0u, total.hi, o), __shfl_xor_sync(~0u, total.lo, o)});
-  }
-  const Pair r = pair_rsqrt(total, a);
+  const Pair r = pair_rsqrt(total, eps, a);
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int v = in_row + i * R;

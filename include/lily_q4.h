@@ -479,9 +479,9 @@ typedef struct {
  *   mx = what lily_mx_quantize makes of y.
  * sum (gets s), y and mx are each optional (NULL), but not all of them absent.  sum and y may each be
  * x or add, with the same stride; no two outputs may be the same.  Both roundings are those of exact
- * arithmetic (to 2^-40 of a value), so neither y nor mx depends on how a row is shared out.  A row's sum of squares
- * has to be below 2^125; products s * (weight + weight_offset) below 2^-126 may lose bits.  A row that is not finite
- * stays by itself.
+ * arithmetic (to 2^-40 of a value, or 2^-148 where y or s * (weight + weight_offset) is small), so neither y nor mx
+ * depends on how a row is shared out.  That holds for all rows of finite numbers and every eps; a row of zeros with eps = 0 is
+ * NaN.  A row that is not finite stays by itself.
  * T: up to 2^30 (larger: LILY_Q4_ERR_UNSUPPORTED).  mx: rows >= T, cols = width; its first T rows are written.
  */
 LILY_Q4_API int lily_add_rms_norm(const lily_rms_norm *op, int32_t T, const void *x, int64_t x_ts,
