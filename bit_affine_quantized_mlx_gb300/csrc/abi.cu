@@ -426,7 +426,7 @@ int lily_add_rms_norm(const lily_rms_norm *op, int32_t T, const void *x, int64_t
   if (!op || T < 0) return LILY_Q4_ERR_INVALID_ARG;
   if (op->width < 8 || op->width > 32768 || op->width % 8) return LILY_Q4_ERR_UNSUPPORTED;
   if (op->dtype != LILY_BF16 && op->dtype != LILY_F16) return LILY_Q4_ERR_UNSUPPORTED;
-  if (!(op->eps >= 0.f) || !(fabsf(op->weight_offset) < HUGE_VALF)) return LILY_Q4_ERR_INVALID_ARG;
+  if (!(op->eps >= 0.f && op->eps < HUGE_VALF) || !(fabsf(op->weight_offset) < HUGE_VALF)) return LILY_Q4_ERR_INVALID_ARG;
   if (op->weight && !aligned(op->weight, 16)) return LILY_Q4_ERR_INVALID_ARG;
   if (!sum && !y && !mx) return LILY_Q4_ERR_INVALID_ARG;
   if (mx) {

@@ -467,7 +467,7 @@ typedef struct {
 typedef struct {
   int32_t width;       /* H: a multiple of 8 (of 32 with `mx`), 8..32768 */
   int32_t dtype;       /* LILY_BF16 or LILY_F16: rows and weights */
-  float eps;           /* added to the mean square */
+  float eps;           /* added to the mean square: 0 or more, finite */
   float weight_offset; /* added to the weights (1 where a checkpoint stores w - 1) */
   const void *weight;  /* [H], 16-byte aligned, or NULL for ones (weight_offset is then unused) */
 } lily_rms_norm;
