@@ -4,10 +4,12 @@
 // (a logit, how many of its equals), and nothing of the vocabulary's size is sorted.  The token is the first in the order
 // of indices whose cumulative weight is above u times the total.
 //
-// Every decision is one between integers: a weight is 2^43 exp((l - max) / T) rounded to a 64-bit integer, with an
-// error of 2^-44 of the largest, so sums do not depend on their order and a comparison falls otherwise
-// than that of the real numbers only within about 1e-12 of a tie.  Such a weight takes some fifty instructions;
-// where fp32 weights with a bound on their error leave the decision in no doubt, they make it instead.
+// Every decision is one between integers: a weight is exp((l - max) / T) as a 64-bit integer, right to 2^-41.5 of itself and
+// rounded to a unit that leaves the row's sum its 61 bits (see set_unit), so sums do not depend on their order.  Equal
+// logits are all rounded the same way: V of them move a sum by V times half a unit, 2^-61 of the sum, and what weighs nothing
+// (below 2^-60 of the largest) by V 2^-60.  A comparison falls otherwise than that of the real numbers only within
+// 1e-12 of the sum, then, at the largest V.  Such a weight takes some fifty instructions; where fp32 weights with a
+// bound on their error leave the decision in no doubt, they make it instead.
 //
 // A cluster of blocks holds a row in its shared memory, each block a run of it, and reads it from there for every
 // pass; sums, histograms and candidates are exchanged by reading the other blocks' shared memory, all blocks
@@ -40,9 +42,10 @@ constexpr int kStep = 128;                  // neighbours that a warp takes at o
 constexpr int kMaxSlice = kSampleMaxVocab / 8 + kStep;
 constexpr int kMaxSteps = kMaxSlice / kStep;
 constexpr int kMaxCluster = 8;
-constexpr float kNoWeight = 44.5f;          // 2^-44.5 and less of the largest weight rounds to nothing
-constexpr float kBinsAOctave = kBins / kNoWeight;
-constexpr int kOneBits = 43;
+constexpr float kNoWeight = 60.f;           // 2^-60 and less of the largest weighs nothing
+constexpr float kBinsAOctave = kBins / 44.5f;  // the last bin takes what is beyond (2^-25 of the sum at most)
+constexpr int kFreeBits = 43;               // units of 2^-43 of the largest, which any row's sum has room for
+constexpr int kListBits = 52;               // and any list's
 constexpr uint32_t kKeyNone = 0x007FFFFFu;  // the key of -infinity
 
 struct SampleArgs {
@@ -82,12 +85,13 @@ __device__ __forceinline__ uint32_t key_of(float l) {
 }
 __device__ __forceinline__ float logit_of(uint32_t key) { return __uint_as_float((key >> 31) ? key ^ 0x80000000u : ~key); }
 
-// What turns a row's logits into weights: x = (max - l) * log2(e) / T, the weight 2^(43 - x).
+// What turns a row's logits into weights: x = (max - l) * log2(e) / T, the weight 2^(bits - x).
 struct Scale {
   float top, hi, lo;  // the largest logit (finite); log2(e) / T as a pair
+  int bits;           // the unit is 2^-bits of the largest weight
 };
 __device__ __forceinline__ float rough_exponent(const Scale &s, float l) { return __fmul_rn(__fsub_rn(s.top, l), s.hi); }
-// 2^(43 - x) to the nearest, 0 from kNoWeight on.  x = n + i/256 + r; 2^-r = 1 - a + a^2 (1/2 - a/6 + a^2/24), a = r ln 2
+// 2^(bits - x) to the nearest, 0 from kNoWeight on.  x = n + i/256 + r; 2^-r = 1 - a + a^2 (1/2 - a/6 + a^2/24), a = r ln 2
 // below 2^-9.5, whose first term is kept as a pair; the product with the table's pair too.
 __device__ __forceinline__ uint64_t weight_of(const Scale &s, float l, const float2 *table) {
   // max - l and what its rounding drops
@@ -115,11 +119,11 @@ __device__ __forceinline__ uint64_t weight_of(const Scale &s, float l, const flo
   const float one = __fadd_rn(hi, 1.f), whole = __fsub_rn(one, 1.f);
   lo = __fadd_rn(lo, __fsub_rn(hi, whole));
   const int32_t units = one < 2.f ? __float_as_int(one) - 0x3F800000 : (__float_as_int(one) - 0x40000000 + 0x400000) * 2;
-  const int64_t w = (int64_t)units * (1 << 26) + __float2int_rn(lo * 0x1p49f);  // units of 2^-49
-  const int drop = 49 - kOneBits + (k >> 8);
-  return (uint64_t)(w + ((int64_t)1 << (drop - 1))) >> drop;
+  const uint64_t w = (uint64_t)((int64_t)units * ((int64_t)1 << 37) + (int64_t)__float2int_rn(lo * 0x1p49f) * 2048);  // 2^-60
+  const int drop = min(63, 60 - s.bits + (k >> 8));
+  return (w + (((uint64_t)1 << drop) >> 1)) >> drop;
 }
-// The same to 2^-29 and one unit, for half of the instructions: the table's entry and 2^-r - 1 in one fp32 number.
+// The same in units of 2^-43, to 2^-29 and one unit, for half of the instructions: the table's entry and 2^-r - 1 in one fp32 number.
 __device__ __forceinline__ uint64_t near_weight(const Scale &s, float l, const float2 *table) {
   const float d = __fsub_rn(s.top, l), b = __fsub_rn(d, s.top);
   const float d_lo = __fsub_rn(__fsub_rn(s.top, __fsub_rn(d, b)), __fadd_rn(l, b));
@@ -276,6 +280,7 @@ struct Row {
   int rank, cluster, first, padded;  // first: index of l[0]; padded: a multiple of kStep
   int turn, hist_turn;
   uint64_t total, off;  // the row's sum of weights to within `off`, once a list has found it
+  bool summed;          // the unit is that of the row's sum
 
   // f(place, logit) for all of the block's logits
   template <typename F>
@@ -297,6 +302,19 @@ struct Row {
     if (at < kList) sh.list[turn][at] = (uint64_t)key_of(v) << 32 | (uint32_t)~(first + i);
   }
 
+  // The unit with which a sum of weights, in largest ones, keeps 61 bits (and below 62, where it is off by less than a half).
+  __device__ __forceinline__ void set_unit(float sum) {
+    scale.bits = min(60, 187 - (int)(__float_as_uint(sum) >> 23)), summed = true;
+  }
+  // The same where nothing else gives the sum: from fp32 weights.
+  __device__ void find_unit() {
+    float sum = 0.f;
+    each([&](int, float v) { sum += fast_weight(scale, v); });
+    uint64_t all = (uint64_t)(sum * 0x1p43f), none = 0;
+    exchange(all, none);
+    set_unit((float)all * 0x1p-43f);
+  }
+
   // Sums over the cluster; every thread gets them.
   __device__ void exchange(uint64_t &a, uint64_t &b) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -316,10 +334,11 @@ struct Row {
 
   // The cluster's histogram (u32 counts or u64 sums) with the cut in it: the bin where the measure, summed from the
   // first bin, reaches `target`, and the sum before it; false if it does not reach it.  The next histogram is cleared.
+  // v: what this thread's bin has.
   template <typename T>
-  __device__ bool find_bin(T target, int &bin, T &before) {
+  __device__ bool find_bin(T target, int &bin, T &before, T &v) {
     cluster_barrier();
-    T v = 0;
+    v = 0;
     each_peer(reinterpret_cast<T *>(sh.hist[hist_turn]) + threadIdx.x, cluster, [&](int, T x) { v += x; });
     hist_turn ^= 1;
     sh.hist[hist_turn][threadIdx.x] = 0;  // the others are done with it
@@ -425,12 +444,21 @@ struct Row {
       filled = false;
       int bin;
       if (MASS) {
-        uint64_t before;
-        if (!find_bin<uint64_t>(target - above, bin, before)) return false;
+        uint64_t before, v;
+        if (!find_bin<uint64_t>(target - above, bin, before, v)) return false;
         above += before;
       } else {
-        uint32_t before;
-        if (!find_bin<uint32_t>((uint32_t)(target - above), bin, before)) return false;
+        uint32_t before, v;
+        const bool found = find_bin<uint32_t>((uint32_t)(target - above), bin, before, v);
+        if (!summed) {  // every token counts as its bin's largest, a sixteenth more than it weighs at most
+          const int t = threadIdx.x;
+          const uint64_t sum = block_scan((uint64_t)((float)v * exp2f(20.f - t * (1.f / kBinsAOctave))), sh);
+          if (t == kBins - 1) sh.found[0] = sum;
+          __syncthreads();
+          set_unit((float)sh.found[0] * 0x1p-20f);
+          __syncthreads();
+        }
+        if (!found) return false;
         above += before;
       }
       if (in.level == 0) in.in_bins(bin, 1, scale);
@@ -633,7 +661,7 @@ __device__ bool Row::select_share(float p, uint64_t target, Cut &cut, int &stepp
   each_peer(sh.counts(hist_turn) + t, cluster, [&](int, uint32_t x) { v += x; });
   hist_turn ^= 1;
   sh.hist[hist_turn][t] = 0;
-  const uint64_t rough = block_scan((uint64_t)((float)v * exp2f(27.f - t * (1.f / kBinsAOctave))), sh);
+  const uint64_t rough = block_scan((uint64_t)((float)v * exp2f(scale.bits - 16 - t * (1.f / kBinsAOctave))), sh);
   if (t == kBins - 1) sh.found[0] = rough;
   __syncthreads();
   // Each weight was rounded to 2^-16.9 of it; ex2, its argument and the bin's exponent add 2^-18: 2^-15 covers that for the
@@ -646,7 +674,7 @@ __device__ bool Row::select_share(float p, uint64_t target, Cut &cut, int &stepp
     if (target == 0) target = max((uint64_t)1, share_of(p, mass(Cut{kKeyNone, 0}), true));
     return select<true>(Members{}, 0, false, target, cut);
   }
-  // a token counts as 61,700 at least: its weight is above 0.9415 of its bin's largest
+  // a token counts as 61,700 at least: its weight is above 0.9415 of its bin's largest (but in the last bin; a list too long ends)
   const uint64_t tokens = block_scan(t <= high ? v : 0, sh);
   if (t == kBins - 1) sh.found[1] = tokens;
   __syncthreads();
@@ -810,6 +838,7 @@ __device__ bool Row::draw(const SampleArgs &a, int64_t b, const Cut &cut, float 
   if (!SUMS_ONLY) return true;
   uint64_t done = 0;
   each_peer(&sh.values[turn][3], cluster, [&](int, uint64_t v) { done += v; });
+  if (MODE == kNear) set_unit((float)total * 0x1p-43f);
   turn ^= 1;
   if (done) cluster_barrier();
   return done != 0;
@@ -927,7 +956,7 @@ __device__ int Row::try_list(ListArgs q, const float (&tops)[2], float u, int32_
   if (bins) {
     // a little below the bins' end, so that rounding leaves none of them out
     q.all = bins >= kBins;
-    const float depth = __fdiv_ru(min(bins, kBins) * (1.00001f / kBinsAOctave), scale.hi);
+    const float depth = __fdiv_ru(q.all ? kNoWeight * 1.00001f : bins * (1.00001f / kBinsAOctave), scale.hi);
     const float from = __fsub_rd(scale.top, depth);
     if (from > least) least = from;
     else q.all = true;
@@ -969,7 +998,10 @@ __device__ int Row::try_list(ListArgs q, const float (&tops)[2], float u, int32_
     // and 31 more by 57 * 2^-24: 4.5e-6 together, below 2^-17.
     float whole = 0.f;
     each_peer(&sh.values[here][1], cluster, [&](int, uint64_t v) { whole += __uint_as_float((uint32_t)v); });
-    total = q.total = (uint64_t)(whole * 0x1p43f), off = q.off = q.total >> 17;
+    set_unit(whole);
+    total = q.total = (uint64_t)(whole * __uint_as_float((uint32_t)(127 + scale.bits) << 23)), off = q.off = q.total >> 17;
+  } else if (!summed) {
+    scale.bits = kListBits;
   }
   if (q.n > kList || q.n == 0) return kNotEnough;
   // The other blocks leave, and make room for the next row's, as soon as the first has read their lists or said that they are
@@ -1065,7 +1097,7 @@ __global__ void __launch_bounds__(kSampleThreads, 2) sample_kernel(SampleArgs a)
   __syncthreads();
   const uint32_t best = __reduce_max_sync(~0u, (uint32_t)sh.warp_sum[lane % kSampleWarps][1]);
   top = logit_of(best);
-  Row row{sh, s_logits, Scale{top, 0.f, 0.f}, rank, a.cluster, first, padded, 1, 0, 0, 0};
+  Row row{sh, s_logits, Scale{top, 0.f, 0.f, kFreeBits}, rank, a.cluster, first, padded, 1, 0, 0, 0, false};
 
   if (best == kKeyNone) {
     if (rank == 0 && t == 0) {
@@ -1142,6 +1174,7 @@ __global__ void __launch_bounds__(kSampleThreads, 2) sample_kernel(SampleArgs a)
     } else if (enough()) {
       return;
     }
+    if (!row.summed && !by_k) row.find_unit();
     uint64_t target = 0;
     if (by_k) {
       row.select<false>(Row::Members{}, 0, false, (uint64_t)k, cut);

@@ -538,9 +538,8 @@ typedef struct {
  * (beyond: as at the end).  token: int32 [B].  prob: fp32 [B] or NULL.  kept: int32 [B] or NULL.
  * Logits of -infinity and NaN are never kept; beside +infinity nothing else is.  A row without a logit to keep gets
  * token -1, prob 0, kept 0 and is recorded for lily_q4_workspace_status as LILY_Q4_ERR_INDEX.
- * Weights are integers in units of 2^-43 of the largest, so results are the same on every run; a decision is
- * that of real numbers unless it is within about 1e-12 of the row's sum of a tie, and tokens below 2^-44 of the
- * largest are never drawn.
+ * Weights are summed as integers, so results are the same on every run; with T up to 2^100 a decision is that of real numbers
+ * unless it is within 1e-12 of the sum of a tie, and tokens below 2^-60 of the largest are never drawn.
  * prob is off by 2^-22 of itself and 2^-43; in rows without a filter, whose sums may be of fp32 weights, by 2^-18 of itself.
  * V: 1..393216, B: up to 2^24 (larger: LILY_Q4_ERR_UNSUPPORTED).  ws: a workspace of at least 256 bytes (its error word is
  * used).
