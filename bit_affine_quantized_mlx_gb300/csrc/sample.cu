@@ -123,7 +123,7 @@ __device__ __forceinline__ uint64_t weight_of(const Scale &s, float l, const flo
   const int drop = min(63, 60 - s.bits + (k >> 8));
   return (w + (((uint64_t)1 << drop) >> 1)) >> drop;
 }
-// The same in units of 2^-43, to 2^-29 and one unit, for half of the instructions: the table's entry and 2^-r - 1 in one fp32 number.
+// The same in units of 2^-43, to 2^-29 and half a unit, for half of the instructions: the table's entry and 2^-r - 1 in one fp32 number.
 __device__ __forceinline__ uint64_t near_weight(const Scale &s, float l, const float2 *table) {
   const float d = __fsub_rn(s.top, l), b = __fsub_rn(d, s.top);
   const float d_lo = __fsub_rn(__fsub_rn(s.top, __fsub_rn(d, b)), __fadd_rn(l, b));
@@ -788,8 +788,8 @@ __device__ bool Row::draw(const SampleArgs &a, int64_t b, const Cut &cut, float 
   const uint64_t place = share_of(u, total, false);
   // Fast weights are off by 1.1e-6 (see try_list), a step's sum by 9 * 2^-24, its conversion by one: below 2^-19 of the
   // total for a border and for the place each.
-  // Near ones are off by 2^-29, and by roundings to units that go either way: 2^12 is over ten times the root of their number.
-  const uint64_t off = MODE == kFast ? (total >> 18) + 2 * kMaxSteps * kMaxCluster : MODE == kNear ? (total >> 28) + (1 << 12) : 0;
+  // Near ones are off by 2^-29 and half a unit, equal ones all the same way: each 2^-29 of the total and half a unit a token.
+  const uint64_t off = MODE == kFast ? (total >> 18) + 2 * kMaxSteps * kMaxCluster : MODE == kNear ? (total >> 28) + usable_count + 1 : 0;
   auto upto = [&](uint64_t m, uint64_t t) { return m + tie_weight * min(t, cut.ties); };
   const uint64_t my_mass = sh.values[turn][0], my_ties = sh.values[turn][2];
   const bool here = upto(mass_before, ties_before) <= place && place < upto(mass_before + my_mass, ties_before + my_ties);

@@ -150,3 +150,10 @@ def test_short_lists(torch):
         us = np.concatenate([[0.0, 0.5], 1 - spread(10, 0, n * w), spread(10, 0, n * w)])
         for kw in (dict(p=0.99999994), dict(k=300), dict(k=n, p=0.99999994), dict(m=1e-12)):
             check(torch, l, "bfloat16", us, **kw)
+
+
+@pytest.mark.parametrize("V,tail", [(151936, -27.25), (393216, -29.5), (393216, -36.25)])
+def test_the_token_in_a_flat_tail(torch, V, tail):
+    """Without a filter, where weights are too small for the sums that are not exact to decide."""
+    w = math.exp(tail)
+    check(torch, flat(V, tail, V - 1), "bfloat16", np.concatenate([spread(30, 0, V * w / (1 + V * w)), [0.0, 0.5]]))
