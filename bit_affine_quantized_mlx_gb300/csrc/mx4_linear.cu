@@ -15,8 +15,8 @@
 // and 128 elements of K are 512 bytes, row r's four at (r % 32) * 16 + (r / 32) * 4, and go to four columns of
 // tensor memory ahead of the products that use them; tcgen05.cp and tcgen05.mma run in the order of their issue.
 //
-// Where there are fewer tiles than half of the SMs, a cluster of up to 8 blocks shares a tile: each takes a
-// part of K, and their sums meet in shared memory in the order of the parts.
+// Where there are tiles for two fifths of the SMs at most, a cluster of up to 8 blocks shares a tile: each takes a
+// part of K, and their sums meet in shared memory in the order of the parts.  Such calls have tiles of 16 tokens (see tile_width).
 //
 // Measured on one GB300, 8-bit rows unless said otherwise: 16 x 151,936 x 2048 29.7 us (5.9 TB/s, 87% of the measured copy
 // rate); 1 x 5120 x 2048 5.2 us (about 1.9 until the first weights and scales are there, 0.7 of products, 1.3 of the
@@ -58,7 +58,8 @@ struct LinShape {
   // A wait on a barrier's parity holds for one phase back.  A warp that copies scales skips the other's PER stages, and it
   // waited for the stage before those; with STAGES > PER the phase before the one it waits for next is over by then.
   static_assert(STAGES > PER, "a parity would be taken for the one two phases on");
-  static_assert(COLS <= 512 && NT * kLinM * 4 <= STAGES * STAGE, "tile does not fit");
+  static constexpr bool SHARED = NT == 16;  // a cluster may share a tile
+  static_assert(COLS <= 512 && (!SHARED || NT * kLinM * 4 <= STAGES * STAGE), "tile does not fit");
 };
 
 struct LinArgs {
@@ -215,9 +216,10 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   auto acc_empty = [&](int i) { return bars + 8 * (2 * S::STAGES + 2 + i); };
   const uint32_t drained = bars + 8 * (2 * S::STAGES + 4);
   const int warp = __shfl_sync(~0u, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-  const int rank = blockIdx.x % a.split, group = blockIdx.x / a.split, groups = gridDim.x / a.split;
+  const int split = S::SHARED ? a.split : 1;
+  const int rank = blockIdx.x % split, group = blockIdx.x / split, groups = gridDim.x / split;
   const int blocks = (a.K + S::KB - 1) / S::KB;
-  const int k_begin = (int)((int64_t)blocks * rank / a.split), k_end = (int)((int64_t)blocks * (rank + 1) / a.split);
+  const int k_begin = (int)((int64_t)blocks * rank / split), k_end = (int)((int64_t)blocks * (rank + 1) / split);
   volatile int *abort = &s_abort;
 
   if (threadIdx.x == 0) {
@@ -432,7 +434,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
       for (int c = 16 * half; c < NT && t0 + c < a.T; c += 32) {
         float v[16];
         tc::tmem_ld16(mine + buf * NT + c, v);
-        if (a.split > 1) {  // one tile: the stages are free, and take the sums
+        if (split > 1) {  // one tile: the stages are free, and take the sums
 #pragma unroll
           for (int j = 0; j < 16; ++j)
             asm volatile("st.shared.f32 [%0], %1;" ::"r"(tiles_at + 4 * ((c + j) * kLinM + row)), "f"(v[j]) : "memory");
@@ -451,17 +453,17 @@ __global__ void __launch_bounds__(kLinThreads, 1)
     }
   }
   __syncwarp();
-  if (a.split > 1) {
+  if (split > 1) {
     cluster_sync();
     const int tile = group, n0 = tile % a.m_tiles * kLinM, t0 = tile / a.m_tiles * NT;
     const int cells = min(NT, a.T - t0) * kLinM;
     if (!*abort) {
-      for (int i = rank * kLinThreads + threadIdx.x; i < cells; i += a.split * kLinThreads) {
+      for (int i = rank * kLinThreads + threadIdx.x; i < cells; i += split * kLinThreads) {
         float v[8], sum = 0.f;  // all are asked for before the first is waited for
 #pragma unroll
-        for (int p = 0; p < 8; ++p) v[p] = p < a.split ? peer_float(tiles_at + 4 * i, p) : 0.f;
+        for (int p = 0; p < 8; ++p) v[p] = p < split ? peer_float(tiles_at + 4 * i, p) : 0.f;
 #pragma unroll
-        for (int p = 0; p < 8; ++p) sum += p < a.split ? v[p] : 0.f;
+        for (int p = 0; p < 8; ++p) sum += p < split ? v[p] : 0.f;
         const int n = n0 + i % kLinM;
         if (n < a.N) store_out(a, t0 + i / kLinM, n, sum);
       }
@@ -532,7 +534,7 @@ static cudaError_t launch_tiles(const lily_mx_mat &W, const lily_mx_mat &x, LinA
   const int64_t tiles = (int64_t)a.m_tiles * ((a.T + NT - 1) / NT);
   if (tiles > INT32_MAX) return cudaErrorInvalidValue;
   a.tiles = (int)tiles;
-  a.split = k_parts((int)tiles, blocks, sms);
+  a.split = S::SHARED ? k_parts((int)tiles, blocks, sms) : 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(a.split > 1 ? a.split * a.tiles : std::min(a.tiles, sms));
   cfg.blockDim = dim3(kLinThreads);
@@ -544,12 +546,14 @@ static cudaError_t launch_tiles(const lily_mx_mat &W, const lily_mx_mat &x, LinA
   attr[1].id = cudaLaunchAttributeClusterDimension;
   attr[1].val.clusterDim.x = a.split, attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 2;
+  cfg.numAttrs = S::SHARED ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, mx4_linear_kernel<BITS, NT>, w_map, x_map, a);
 }
 
 // Tokens a tile.  What a tile costs goes with the rows that its stages bring to shared memory and the products read there,
 // 128 of weights and NT of tokens, so the width is the one with the least of rows times rounds of tiles over the SMs.
+// A wider tile costs more in one round, so one is taken only where the width before it needs a second: there are more tiles than SMs of
+// that, and, as no width is more than twice the one before, more than half as many of the wider, too many for clusters.
 // (3001 x 2048 x 4096 of 4-bit rows: 16.4 us with 192, two rounds of which the second is 68% full; 15.5 with 160.)
 static int tile_width(int64_t T, int64_t m_tiles, int64_t sms) {
   int best = 16;
