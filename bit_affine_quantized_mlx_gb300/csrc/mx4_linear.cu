@@ -39,6 +39,7 @@ constexpr int kSfAhead = 3;  // fetches of scales of either warp that are on the
 template <int BITS, int NT>
 struct LinShape {
   static constexpr int KB = BITS == 8 ? 128 : 256;          // elements of K a stage: rows of 128 bytes
+  __host__ __device__ static constexpr int k_blocks(int K) { return K / KB + (K % KB != 0); }  // (K + KB - 1 may pass 2^31)
   static constexpr int GROUPS = KB / 128;                    // of 128 elements: one word of scales a row
   static constexpr int XSF = (NT + 127) / 128;               // 512-byte blocks of the tokens' scales a group
   static constexpr int W_BYTES = kLinM * 128, X_BYTES = NT * 128;
@@ -218,7 +219,7 @@ __global__ void __launch_bounds__(kLinThreads, 1)
   const int warp = __shfl_sync(~0u, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int split = S::SHARED ? a.split : 1;
   const int rank = blockIdx.x % split, group = blockIdx.x / split, groups = gridDim.x / split;
-  const int blocks = (a.K + S::KB - 1) / S::KB;
+  const int blocks = S::k_blocks(a.K);
   const int k_begin = (int)((int64_t)blocks * rank / split), k_end = (int)((int64_t)blocks * (rank + 1) / split);
   volatile int *abort = &s_abort;
 
@@ -529,7 +530,7 @@ static cudaError_t launch_tiles(const lily_mx_mat &W, const lily_mx_mat &x, LinA
   if (!encode(&w_map, W.codes, W.rows, W.cols, 4, BITS == 8, kLinM) ||
       !encode(&x_map, x.codes, x.rows, x.cols, BITS, false, NT))
     return cudaErrorInvalidValue;
-  const int sms = std::max(1, sm_count()), blocks = (a.K + S::KB - 1) / S::KB;
+  const int sms = std::max(1, sm_count()), blocks = S::k_blocks(a.K);
   a.m_tiles = (a.N + kLinM - 1) / kLinM;
   const int64_t tiles = (int64_t)a.m_tiles * ((a.T + NT - 1) / NT);
   if (tiles > INT32_MAX) return cudaErrorInvalidValue;

@@ -132,3 +132,22 @@ def test_sampling_of_many_rows(torch):  # noqa: F811
     q4.lily_sample(q4.Sampling(top_p=torch.full((B,), 0.5, device="cuda")), l, u, token, ws=q4.new_workspace(256))
     want = {(i, j): plain_row(_np(some[i]), 1.0, 0, 0.5, 0.0, float(u[j]))[0] for i in range(7) for j in range(5)}
     assert token.tolist() == [want[b % 7, b % 5] for b in range(B)]
+
+
+@pytest.mark.parametrize("bits", [8, 4])
+@pytest.mark.parametrize("K", [(1 << 31) - 128, (1 << 31) - 256])
+def test_product_of_the_longest_rows(torch, K, bits):  # noqa: F811
+    """Zeros but for a few places, whose products are exact."""
+    W, x = q4.DeviceMX.new(2, K, 4), q4.DeviceMX.new(1, K, bits)
+    W.scales.fill_(127)
+    x.scales.fill_(127)
+    at = [0, 129, 1 << 20, (1 << 30) - 1, 1 << 30, K - 257, K - 130, K - 1]
+    for i, k in enumerate(at):  # 2^(i % 3) in x, 1 and 2^(i % 2) in W
+        one = lambda m, row, e: m.codes[row, k // 2].add_((2 + 2 * e) << (4 * (k % 2))) if m.bits == 4 else m.codes[row, k].fill_((7 + e) << 3)
+        one(x, 0, i % 3)
+        one(W, 0, 0)
+        one(W, 1, i % 2)
+    out, ws = torch.empty((1, 2), device="cuda"), q4.new_workspace(256)
+    q4.lily_mx4_linear(W, x, out, ws=ws)
+    assert q4.lily_q4_workspace_status(ws) == q4.OK
+    assert out.tolist() == [[sum(2.0 ** (i % 3) for i in range(len(at))), sum(2.0 ** (i % 3 + i % 2) for i in range(len(at)))]]
