@@ -4,8 +4,8 @@
 // thread takes eight neighbours (16 bytes of a 16-bit row), so a block of 32 is in four neighbouring
 // lanes and its largest magnitude takes two exchanges.
 //
-// Measured on one GB300: 8192 rows of 2048 with the addition and all outputs 26.8 us (5.6 TB/s, 83% of the measured copy rate);
-// without the addition, to 8 bits alone, 19.6 us (2.6 TB/s: bound by the issue of some 30 instructions an element);
+// Measured on one GB300: 8192 rows of 2048 with the addition and all outputs 26.0 us (5.8 TB/s, 85% of the measured copy rate);
+// without the addition, to 8 bits alone, 18.7 us (2.7 TB/s: bound by the issue of some 30 instructions an element);
 // one row 2.0 us (a launch).  151,936 x 2048 of bf16 to 4 bits 126 us (6.2 TB/s), back 114 us (6.9 TB/s).
 #include <algorithm>
 
@@ -91,7 +91,7 @@ __device__ __forceinline__ Pair pair_rsqrt(Pair total, float eps, const NormArgs
 // An odd number is no tie of a shorter format, and lies on the same side of each as hi + lo.
 __device__ __forceinline__ float to_odd(float hi, float lo) {
   const uint32_t b = __float_as_uint(hi);
-  if ((b & 1) || lo == 0.f || hi == 0.f) return hi;
+  if ((b & 1) || lo == 0.f) return hi;  // (a zero has no rest)
   return __uint_as_float((__float_as_uint(lo) ^ b) >> 31 ? b - 1 : b + 1);
 }
 
@@ -107,7 +107,8 @@ __device__ __forceinline__ void scale_exactly(float (&s)[8], const float (&w)[8]
     const float hi = __fmul_rn(p, r.hi);
     const float lo = __fmaf_rn(p_lo, r.hi, __fmaf_rn(p, r.lo, __fmaf_rn(p, r.hi, -hi)));
     const float y = __fadd_rn(hi, lo);
-    s[j] = hi == 0.f ? hi : to_odd(y, __fsub_rn(lo, __fsub_rn(y, hi)));  // (a sum of zeros would lose the sign)
+    const float odd = to_odd(y, __fsub_rn(lo, __fsub_rn(y, hi)));
+    s[j] = __uint_as_float(__float_as_uint(odd) | (__float_as_uint(hi) & 0x80000000u));  // (a sum of zeros loses it)
   }
 }
 // The same as 16-bit numbers, by plain fp32 products with a root a little smaller and one a little larger: rounding keeps the
@@ -141,7 +142,7 @@ __device__ __forceinline__ uint4 scale_eight(const uint4 &s, const uint4 &w, flo
 // In range nothing counts that fp32 cannot hold: what a square and its remainder lose is 2^-149 at most, of up to 2^15 squares
 // 2^-54 of a sum of 2^-80 or, whatever the sum is, 2^-49 of an eps of 2^-100.  (Sums of fp16 squares are 2^-48 to 2^47.)  Large rows go
 // to 2^40 instead of 1, so that their small elements do not run out of bits.  (What asking takes: 8192 rows of 2048 with all
-// outputs 26.5 -> 26.8 us, to 8 bits alone 18.9 -> 19.6.)
+// outputs 25.8 -> 26.0 us, to 8 bits alone 18.1 -> 18.7.)
 __device__ __forceinline__ bool out_of_range(Pair total, float eps) {
   return !(total.hi < 0x1p100f) || (eps < 0x1p-100f && total.hi < 0x1p-80f);
 }
