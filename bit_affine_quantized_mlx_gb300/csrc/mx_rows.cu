@@ -78,7 +78,7 @@ __device__ __forceinline__ Pair pair_rsqrt(Pair total, float eps, const NormArgs
   m.lo = __fmaf_rn(total.hi, a.inv_lo, __fmaf_rn(total.lo, a.inv_hi, m.lo));
   m = pair_add(m, Pair{eps, 0.f});
   // an even power of two goes to the end, so that the root's square has a remainder whatever eps is
-  const int even = ((int)(__float_as_uint(m.hi) >> 23) - 127) & ~1;
+  const int even = (max(1, (int)(__float_as_uint(m.hi) >> 23)) - 127) & ~1;
   const float by = __uint_as_float((uint32_t)(127 - even) << 23), back = __uint_as_float((uint32_t)(127 - even / 2) << 23);
   m.hi = __fmul_rn(m.hi, by), m.lo = __fmul_rn(m.lo, by);
   // r (1 + e / 2), e = 1 - m r^2: what is left is 3/8 e^2, 2^-43 at the root's accuracy of 2^-22

@@ -112,3 +112,17 @@ def test_rows_that_are_not_finite_stay_by_themselves(torch):
     y = torch.empty_like(x)
     q4.lily_add_rms_norm(q4.RMSNorm(torch.ones(512, dtype=torch.bfloat16, device="cuda"), eps=0.0), x, y=y)
     assert bool((y[[0, 2, 4, 5]] == 1).all()) and bool(y[[1, 3]].isnan().any(1).all())
+
+
+@pytest.mark.parametrize("dtype", ["bfloat16", "float16"])
+@pytest.mark.parametrize("eps", [1e-45, 1e-42, 1e-38, 1e-20, 1e30])
+@pytest.mark.parametrize("H", [64, 4096])
+def test_rows_of_zeros(torch, H, eps, dtype):
+    """Zeros with any eps above 0, beside a row that is not."""
+    x = torch.zeros((3, H), dtype=getattr(torch, dtype), device="cuda")
+    x[0], x[2] = 1.0, -0.0
+    y = torch.full_like(x, 7.0)
+    q4.lily_add_rms_norm(q4.RMSNorm(torch.ones(H, dtype=x.dtype, device="cuda"), eps=eps), x, y=y)
+    assert bool((y[1:] == 0).all()) and bool(y[2].signbit().all()) and not bool(y[1].signbit().any())
+    one = plain.round16(np.ones(1) / np.sqrt(1.0 + np.float64(np.float32(eps))), "bf16" if dtype == "bfloat16" else "fp16")
+    assert np.array_equal(_np(y[0]), np.repeat(one, H))
