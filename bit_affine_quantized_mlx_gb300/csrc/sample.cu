@@ -22,12 +22,12 @@
 //  - the long way: a histogram of the distance from the largest logit, refined inside the bin of the cut until few
 //    candidates are left, and sums of exact weights.
 //
-// Measured on one GB300, fp32 rows of 151,936, one row / 16 / 64: the largest 6.8 / 9.6 / 19 us, no filter 11 / 15 / 30 to 40
-// (by how many rows leave fp32 sums in doubt), top_k 20 10.5 / 13.4 / 27.5, top_p 0.9 at T = 0.8 12.2 / 16.3 / 34; over a
-// flat bulk top_p 0.95 at T = 1.2 (26,634 tokens kept) 47 / 60 / 134, top_k 1000 27 / 33 / 70.  Reading takes 0.1 us a row:
+// Measured on one GB300, fp32 rows of 151,936, one row / 16 / 64: the largest 6.8 / 9.6 / 19.8 us, no filter 11 / 15 to 21 / 30 to 46
+// (by how many rows leave fp32 sums in doubt), top_k 20 10.5 / 13.4 / 27.6, top_p 0.9 at T = 0.8 12.3 / 16.4 / 34.6; over a
+// flat bulk top_p 0.95 at T = 1.2 (26,634 tokens kept) 47 / 61 / 135, top_k 1000 27 / 34 / 72.  Reading takes 0.1 us a row:
 // what bounds one row is the chain of its passes and exchanges (a microsecond a cluster barrier and what goes
 // with it; the pass of exact weights over a flat bulk 11), many rows the issue of a pass's instructions and the
-// rounds of blocks, two an SM.
+// rounds of blocks, two an SM.  (Of a thread's state some 450 bytes are spilled: 64 registers is what two blocks an SM leave.)
 #include <algorithm>
 
 #include "mx_device.cuh"
@@ -44,7 +44,7 @@ constexpr int kMaxSteps = kMaxSlice / kStep;
 constexpr int kMaxCluster = 8;
 constexpr float kNoWeight = 60.f;           // 2^-60 and less of the largest weighs nothing
 constexpr float kBinsAOctave = kBins / 44.5f;  // the last bin takes what is beyond (2^-25 of the sum at most)
-constexpr int kFreeBits = 43;               // units of 2^-43 of the largest, which any row's sum has room for
+constexpr int kFreeBits = 43;               // units of 2^-43 of the largest: any row's sum has room for them
 constexpr int kListBits = 52;               // and any list's
 constexpr uint32_t kKeyNone = 0x007FFFFFu;  // the key of -infinity
 
@@ -123,7 +123,7 @@ __device__ __forceinline__ uint64_t weight_of(const Scale &s, float l, const flo
   const int drop = min(63, 60 - s.bits + (k >> 8));
   return (w + (((uint64_t)1 << drop) >> 1)) >> drop;
 }
-// The same in units of 2^-43, to 2^-29 and half a unit, for half of the instructions: the table's entry and 2^-r - 1 in one fp32 number.
+// The same to 2^-29 and half a unit, for half of the instructions: the table's entry and 2^-r - 1 in one fp32 number.
 __device__ __forceinline__ uint64_t near_weight(const Scale &s, float l, const float2 *table) {
   const float d = __fsub_rn(s.top, l), b = __fsub_rn(d, s.top);
   const float d_lo = __fsub_rn(__fsub_rn(s.top, __fsub_rn(d, b)), __fadd_rn(l, b));
@@ -139,8 +139,8 @@ __device__ __forceinline__ uint64_t near_weight(const Scale &s, float l, const f
   // in units of 2^-31: what the entry's first part has, exactly, and the rest
   const uint32_t first = (uint32_t)((__float_as_int(t.x) & 0x7FFFFF) | 0x800000) << (__float_as_int(t.x) >> 23 == 127 ? 8 : 7);
   const uint32_t w = first + (uint32_t)__float2int_rn(__fmaf_rn(t.x, -less, t.y) * 0x1p31f);
-  const int n = k >> 8;
-  return (((uint64_t)w << 13 >> n) + 1) >> 1;
+  const int drop = min(63, 61 - s.bits + (k >> 8));
+  return (((uint64_t)w << 31 >> drop) + 1) >> 1;
 }
 // 2^-x in fp32, 0 from kNoWeight on: 2^-22 relative, and what the rounding of max - l does, 2^-24 x ln 2.
 __device__ __forceinline__ float fast_weight(const Scale &s, float l) {
@@ -838,7 +838,7 @@ __device__ bool Row::draw(const SampleArgs &a, int64_t b, const Cut &cut, float 
   if (!SUMS_ONLY) return true;
   uint64_t done = 0;
   each_peer(&sh.values[turn][3], cluster, [&](int, uint64_t v) { done += v; });
-  if (MODE == kNear) set_unit((float)total * 0x1p-43f);
+  if (MODE == kFast) set_unit((float)total * 0x1p-43f);  // (for those that follow)
   turn ^= 1;
   if (done) cluster_barrier();
   return done != 0;
