@@ -478,7 +478,7 @@ typedef struct {
  *   y = s / sqrt(mean(s^2) + eps) * (weight + weight_offset) (rounded to dtype);
  *   mx = what lily_mx_quantize makes of y.
  * sum (gets s), y and mx are each optional (NULL), but not all of them absent.  sum and y may each be
- * x or add, with the same stride; no two outputs may be the same.  Both roundings are those of exact
+ * x or add, with the same stride; outputs overlap neither one another nor, otherwise, what is read.  Both roundings are those of exact
  * arithmetic (to 2^-40 of a value, or 2^-148 where y or s * (weight + weight_offset) is small), so neither y nor mx
  * depends on how a row is shared out.  That holds for all rows of finite numbers and every eps; a row of zeros with eps = 0 is
  * NaN.  A row that is not finite stays by itself.
